@@ -423,6 +423,146 @@ INV_API int prefill_layer(const inv_layer_config* cfg, const inv_layer_weights* 
                           void* workspace, size_t ws_bytes, inv_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Paged INT16 KV cache ([HEAL] section 1, the codes and scales of the slot
+ * cache above).  Codes int16 [n_pages][n_kv_heads][page_size][128], scales
+ * fp32 [n_pages][n_kv_heads][page_size], separately for K and V.  page_size is
+ * a power of two from 16 to 256.  Position p of sequence i lives in page
+ * page_table[i * ld_table + p / page_size] at offset p % page_size; sequences
+ * may share pages that neither of them appends to.
+ *
+ * Ragged batches (kv_append_paged and attn_paged take the same descriptors):
+ *   q_start : int32 [n_seqs + 1], ascending; the new tokens of sequence i are
+ *             the rows q_start[i] .. q_start[i+1] - 1 of the call.  A sequence
+ *             may have none.  Rows before q_start[0] and from q_start[n_seqs]
+ *             on belong to no sequence: nothing is computed for them and their
+ *             outputs are left as they were (a batch padded to a captured
+ *             graph's size).
+ *   len     : int32 [n_seqs], positions of sequence i after the call, its new
+ *             tokens included: row r is at position len[i] - (q_start[i+1] - r)
+ *             (not read for a sequence without new tokens).
+ *   page_table : int32 [n_seqs][ld_table]; only the entries of the positions
+ *             0 .. len[i] - 1 are read.
+ * A sequence whose len is smaller than its number of new tokens or beyond the
+ * call's bounds, and a page number outside the cache, record
+ * INV_ERR_INVALID_ARG; the rows concerned are skipped (attn_paged: a row that
+ * reaches a bad page gets unspecified finite values).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int16_t* k;
+  int16_t* v;
+  float* k_scale;
+  float* v_scale;
+  int n_pages;
+  int n_kv_heads;
+  int page_size;
+  int head_dim;
+} inv_paged_kv_cache;
+
+/*
+ * kv_append_paged -- the attention inputs of new tokens, in one pass over the
+ * QKV projection's fp32 output:
+ *   q, k heads (with gains): y = (x r) g, r = fl32(1 / sqrt(sum_d x_d^2 / 128
+ *              + eps)) with the sum, quotient and root in 64 bits, so that r
+ *              does not depend on an order of summation; each of q_gain and
+ *              k_gain (fp32 [128]) may be NULL: no norm of those heads;
+ *   q, k heads: rotary embedding as in decode_layer (rotate-half, pairs
+ *              (i, i+64), the row's table entries, one fp32 rounding per
+ *              product and sum);
+ *   k, v heads: quantised as kv_quant_int16 into the row's place in its page.
+ * Without gains the bits are those of decode_layer's QKV step on the same
+ * fp32 projections.
+ *   qkv    : fp32 [T][ld_qkv], a row holds q (n_heads x 128), k, v (n_kv_heads
+ *            x 128 each); ld_qkv % 4 == 0, 16-byte aligned.
+ *   q_out  : fp32 [T][n_heads][128], 8-byte aligned; may not overlap qkv.
+ *   rope_cos, rope_sin : fp32 [max_pos][64]; a position >= max_pos is an
+ *            INV_ERR_INVALID_ARG of its row.
+ * Errors: INV_ERR_INVALID_ARG; INV_ERR_UNSUPPORTED_SHAPE (head_dim != 128,
+ * page_size, n_heads not a multiple of n_kv_heads).
+ */
+INV_API int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads, const inv_paged_kv_cache* cache,
+                            const int32_t* page_table, int64_t ld_table, int n_seqs, const int32_t* q_start,
+                            const int32_t* len, const float* rope_cos, const float* rope_sin, int max_pos,
+                            const float* q_gain, const float* k_gain, double eps, float* q_out, inv_stream stream);
+
+/*
+ * attn_paged -- causal attention of each sequence's new tokens over its pages
+ * (one token: decode; a few: drafted tokens; many: a prefill chunk; any mix of
+ * these in one call).  The row at position p attends keys 0..p:
+ *   out = sum_j softmax_j(sigma q . K~_j) V~_j,  K~_j = s_K,j code_j.
+ * Batch-invariant ([BI] Attention): a row's bits depend on its own q and keys
+ * only -- not on the other rows, on how many tokens of its sequence are in the
+ * call, nor on the page size or the pages' places.  Arithmetic of a row:
+ *   q 2^e (exact, e per row and head) and w 2^E are split into binary16 hi +
+ *   lo; code / 2 = hi + lo with hi = 32 round-down(code / 64), both exact;
+ *   products hi lo + lo hi, then hi hi, accumulate in fp32 on the tensor cores
+ *   over blocks of INV_PAGED_BLOCK keys at absolute positions (lo lo, below
+ *   2^-20 of a product, is dropped);
+ *   blocks are joined by a running maximum inside segments of
+ *   INV_PAGED_SEGMENT keys, and segments, in ascending order, the same way.
+ *   q        : fp32 [T][ld_q], n_heads x 128 used; ld_q % 4 == 0, 16-byte aligned.
+ *   out      : fp32 [T][n_heads][128]; out_hi/out_lo: binary16 split of out
+ *              (both NULL or both non-NULL).
+ *   max_q_bound : host upper bound on the new tokens of a sequence (<= 0: T).
+ *   max_len_bound : host upper bound on every len[i] (<= 0: ld_table *
+ *              page_size).  The bounds size the launch and the workspace only.
+ *   softmax_scale : sigma >= 0, finite.
+ *   workspace: >= attn_paged_workspace_size(...) bytes for the resolved bounds,
+ *              16-byte aligned (may be NULL if that is 0).  Calls that overlap
+ *              on the GPU need separate workspaces.
+ * Errors: INV_ERR_INVALID_ARG; INV_ERR_UNSUPPORTED_SHAPE unless head_dim == 128,
+ * page_size as above and n_heads / n_kv_heads is an integer from 1 to 16;
+ * INV_ERR_WORKSPACE.  Device: INV_ERR_TIMEOUT, INV_ERR_RANGE (out split
+ * overflow).
+ */
+#define INV_PAGED_BLOCK 128
+#define INV_PAGED_SEGMENT 512
+INV_API size_t attn_paged_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int max_q_bound,
+                                         int max_len_bound);
+INV_API int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged_kv_cache* cache,
+                       const int32_t* page_table, int64_t ld_table, int n_seqs, const int32_t* q_start,
+                       const int32_t* len, int max_q_bound, int max_len_bound, float softmax_scale, float* out,
+                       uint16_t* out_hi, uint16_t* out_lo, void* workspace, size_t ws_bytes, inv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * softmax_rows -- probs[r][j] = exp(t_j - max t) / sum exp(t_j - max t) with
+ * t_j = logits[r][j] * inv_temperature, in fp32, one fixed reduction order per
+ * n (batch-invariant).  -inf logits get probability 0; a row of nothing but
+ * -inf gets zeros.  probs may be logits (same pointer and ld).
+ *   logits : fp32 [rows][ld], probs : fp32 [rows][ld_p], the first n used.
+ *   inv_temperature : finite, > 0.
+ * Errors: INV_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------ */
+INV_API int softmax_rows(const float* logits, int rows, int n, int64_t ld, float inv_temperature, float* probs,
+                         int64_t ld_p, inv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_verify -- speculative sampling's verification of drafted tokens.  For
+ * sequence b with drafts x_0 .. x_{m-1} (m = n_draft[b], or max_draft when
+ * n_draft is NULL), target rows p_0 .. p_m and draft rows q_0 .. q_{m-1}:
+ *   draft i is accepted iff drafts 0..i-1 are and u_accept_i q_i(x_i) <
+ *   p_i(x_i); k = number accepted.  The next token has the weights
+ *   max(p_k - q_k, 0) if k < m, else p_m: the lowest j whose running sum
+ *   exceeds u_sample times the total.  Where every weight is 0 (k < m and
+ *   p_k <= q_k everywhere) the weights are p_k.
+ * Comparisons, weights, running sums and totals are in 64 bits.  Without draft
+ * probabilities (draft NULL: tokens looked up, not sampled) q_i is 1 at x_i
+ * and 0 elsewhere.  No positive weight at all gives the token -1.
+ *   target : fp32 rows (b, i) at target + (b (max_draft + 1) + i) ld_target.
+ *   draft  : fp32 rows (b, i) at draft + (b max_draft + i) ld_draft, or NULL.
+ *   draft_tokens : int32 [B][max_draft];  u_accept : fp32 [B][max_draft],
+ *   u_sample : fp32 [B], in [0, 1).
+ *   tokens : int32 [B][max_draft + 1]: x_0 .. x_{k-1}, the next token, then -1.
+ *   n_accepted : int32 [B]: k.
+ * Errors: INV_ERR_INVALID_ARG.  Device: INV_ERR_INVALID_ARG for a draft token
+ * outside [0, vocab) or n_draft outside [0, max_draft]; that sequence gets
+ * n_accepted 0 and tokens -1.
+ * ------------------------------------------------------------------------ */
+INV_API int spec_verify(const float* target, int64_t ld_target, const float* draft, int64_t ld_draft, int B,
+                        int max_draft, int vocab, const int32_t* draft_tokens, const int32_t* n_draft,
+                        const float* u_accept, const float* u_sample, int32_t* tokens, int32_t* n_accepted,
+                        inv_stream stream);
+
+/* ------------------------------------------------------------------------
  * rope_tables -- model constants for the rotary embedding of decode_layer:
  *   cos_out[p][i] = fl32(cos(p theta_i)), sin_out[p][i] = fl32(sin(p theta_i)),
  *   theta_i = base^(-2i/128), i < 64, 0 <= p < max_pos, evaluated in double
