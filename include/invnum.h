@@ -493,10 +493,10 @@ INV_API int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads
  * only -- not on the other rows, on how many tokens of its sequence are in the
  * call, nor on the page size or the pages' places.  Arithmetic of a row:
  *   q 2^e (exact, e per row and head) and w 2^E are split into binary16 hi +
- *   lo; code / 2 = hi + lo with hi = 32 round-down(code / 64), both exact;
+ *   lo; code / 2 = hi + lo with hi = rn16(code / 2), both exact;
  *   products hi lo + lo hi, then hi hi, accumulate in fp32 on the tensor cores
- *   over blocks of INV_PAGED_BLOCK keys at absolute positions (lo lo, below
- *   2^-20 of a product, is dropped);
+ *   over blocks of INV_PAGED_BLOCK keys at absolute positions (lo lo, at most
+ *   2^-22 of a product, is dropped);
  *   blocks are joined by a running maximum inside segments of
  *   INV_PAGED_SEGMENT keys, and segments, in ascending order, the same way.
  *   q        : fp32 [T][ld_q], n_heads x 128 used; ld_q % 4 == 0, 16-byte aligned.

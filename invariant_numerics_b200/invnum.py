@@ -43,6 +43,11 @@ class KVCacheStruct(C.Structure):
                 ("max_len", _i), ("head_dim", _i)]
 
 
+class PagedKVCacheStruct(C.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("n_pages", _i), ("n_kv_heads", _i),
+                ("page_size", _i), ("head_dim", _i)]
+
+
 class LayerConfigStruct(C.Structure):
     _fields_ = [("hidden", _i), ("n_heads", _i), ("n_kv_heads", _i), ("head_dim", _i), ("ffn", _i),
                 ("max_pos", _i), ("eps", _f), ("softmax_scale", _f)]
@@ -83,6 +88,13 @@ _SIGS = {
     "prefill_layer_workspace_size": (_sz, [C.POINTER(LayerConfigStruct), _i, _i]),
     "prefill_layer": (_i, [C.POINTER(LayerConfigStruct), C.POINTER(LayerWeightsStruct), C.POINTER(KVCacheStruct),
                            _p, _i, _i, _i, _i, _p, _p, _sz, _p]),
+    "kv_append_paged": (_i, [_p, _i64, _i, _i, C.POINTER(PagedKVCacheStruct), _p, _i64, _i, _p, _p, _p, _p, _i, _p, _p,
+                             _d, _p, _p]),
+    "attn_paged_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_paged": (_i, [_p, _i64, _i, _i, C.POINTER(PagedKVCacheStruct), _p, _i64, _i, _p, _p, _i, _i, _f, _p, _p, _p,
+                        _p, _sz, _p]),
+    "softmax_rows": (_i, [_p, _i, _i, _i64, _f, _p, _i64, _p]),
+    "spec_verify": (_i, [_p, _i64, _p, _i64, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p]),
     "rope_tables": (_i, [_i, _d, _p, _p, _p]),
     "embed_gather": (_i, [_p, _i, _i, _p, _i, _p, _p]),
     "argmax_rows": (_i, [_p, _i, _i, _i64, _p, _p]),
@@ -338,6 +350,180 @@ def rmsnorm_bi(x, gamma, eps, want_y=True, want_split=False, stream=None):
     if want_y and want_split:
         return y, hi, lo
     return y if want_y else (hi, lo)
+
+
+# ------------------------------------------- paged cache, draft verification --
+
+def _same_device(x, *others):
+    """The device of x, which must be the current one and hold the others too
+    (the C call launches on the current device's stream)."""
+    d = x.device
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors are on different devices ({d}, {t.device})")
+    return d
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor of the stream the call runs on: memory that is
+    freed after the call is reused behind it on that stream only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows_of(t, name, width=None):
+    """fp32 [rows, width] with contiguous rows: its row stride."""
+    _need(t, torch.float32, name, contiguous=False)
+    if t.dim() != 2 or (width is not None and t.shape[1] != width) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, {width if width is not None else 'n'}] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+class PagedKVCache:
+    """INT16 KV cache in pages: codes [n_pages, n_kv_heads, page_size, 128], scales fp32 [n_pages, n_kv_heads,
+    page_size].  Wraps four tensors; `empty` allocates a zeroed pool."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        _need(k, torch.int16, "k"), _need(v, torch.int16, "v")
+        _need(k_scale, torch.float32, "k_scale"), _need(v_scale, torch.float32, "v_scale")
+        if k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+            raise ValueError("a paged cache is codes [n_pages, n_kv_heads, page_size, 128] and scales of its first "
+                             "three dims, for k and v")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, device="cuda"):
+        codes = lambda: torch.zeros((n_pages, n_kv_heads, page_size, HEAD_DIM), dtype=torch.int16, device=device)
+        scale = lambda: torch.zeros((n_pages, n_kv_heads, page_size), dtype=torch.float32, device=device)
+        return cls(codes(), codes(), scale(), scale())
+
+    def struct(self) -> PagedKVCacheStruct:
+        return PagedKVCacheStruct(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                                  self.v_scale.data_ptr(), self.n_pages, self.n_kv_heads, self.page_size,
+                                  self.head_dim)
+
+
+def _ragged(cache, page_table, q_start, lens):
+    """Checks the descriptors of a ragged batch; the number of sequences."""
+    for t, name in ((page_table, "page_table"), (q_start, "q_start"), (lens, "lens")):
+        _need(t, torch.int32, name)
+    n = lens.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != n or lens.dim() != 1 or q_start.shape != (n + 1,):
+        raise ValueError("page_table [n, pages], q_start [n + 1] and lens [n] must agree on the number of sequences")
+    _same_device(lens, page_table, q_start, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    return n
+
+
+def kv_append_paged(qkv, cache: PagedKVCache, page_table, q_start, lens, rope_cos, rope_sin, q_gain=None, k_gain=None,
+                    eps=1e-6, q_out=None, stream=None):
+    """fp32 qkv [T, (Hq + 2 Hkv) * 128] of the new tokens of a ragged batch -> q fp32 [T, Hq, 128] (normed where
+    q_gain is given, rotated); K (normed where k_gain is given, rotated) and V go to the cache.  Without q_out, the
+    rows of no sequence are unspecified."""
+    n = _ragged(cache, page_table, q_start, lens)
+    ld = _rows_of(qkv, "qkv")
+    _need(rope_cos, torch.float32, "rope_cos"), _need(rope_sin, torch.float32, "rope_sin")
+    T, Hq = qkv.shape[0], qkv.shape[1] // HEAD_DIM - 2 * cache.n_kv_heads
+    if Hq <= 0 or qkv.shape[1] % HEAD_DIM:
+        raise ValueError("qkv must hold n_heads + 2 * n_kv_heads heads of 128")
+    if rope_cos.dim() != 2 or rope_cos.shape[1] != HEAD_DIM // 2 or rope_sin.shape != rope_cos.shape:
+        raise ValueError("rope_cos and rope_sin must be [max_pos, 64]")
+    for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if g is not None and _need(g, torch.float32, name).shape != (HEAD_DIM,):
+            raise ValueError(f"{name} must be [128]")
+    _same_device(lens, qkv, rope_cos, rope_sin, q_gain, k_gain, q_out)
+    if q_out is None:
+        q_out = _new((T, Hq, HEAD_DIM), torch.float32, qkv.device, stream)
+    elif _need(q_out, torch.float32, "q_out").shape != (T, Hq, HEAD_DIM):
+        raise ValueError(f"q_out must be [{T}, {Hq}, 128]")
+    cs = cache.struct()
+    _check("kv_append_paged",
+           lib.kv_append_paged(_ptr(qkv), ld, T, Hq, C.byref(cs), _ptr(page_table), page_table.shape[1], n,
+                               _ptr(q_start), _ptr(lens), _ptr(rope_cos), _ptr(rope_sin), rope_cos.shape[0],
+                               _ptr(q_gain), _ptr(k_gain), float(eps), _ptr(q_out), _stream(stream)))
+    return q_out
+
+
+def attn_paged_workspace_size(T: int, n_seqs: int, n_heads: int, n_kv_heads: int, max_q_bound: int,
+                              max_len_bound: int) -> int:
+    return lib.attn_paged_workspace_size(T, n_seqs, n_heads, n_kv_heads, max_q_bound, max_len_bound)
+
+
+def attn_paged(q, cache: PagedKVCache, page_table, q_start, lens, softmax_scale, max_q_bound=None, max_len_bound=None,
+               out=None, want_split=False, workspace=None, stream=None):
+    """Causal attention of a ragged batch's new tokens over their pages: q fp32 [T, Hq, 128] -> out fp32 [T, Hq, 128]
+    (and hi/lo if want_split).  Without out, the rows of no sequence are unspecified."""
+    n = _ragged(cache, page_table, q_start, lens)
+    _need(q, torch.float32, "q", contiguous=False)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != HEAD_DIM):
+        raise ValueError("q must be [T, n_heads, 128] with contiguous rows")
+    T, Hq, _ = q.shape
+    ld = q.stride(0) if T > 1 else Hq * HEAD_DIM
+    room = page_table.shape[1] * cache.page_size
+    mq = T if max_q_bound is None or max_q_bound <= 0 else min(int(max_q_bound), T)
+    mlb = room if max_len_bound is None or max_len_bound <= 0 else min(int(max_len_bound), room)
+    _same_device(lens, q, out, workspace)
+    if out is None:
+        out = _new((T, Hq, HEAD_DIM), torch.float32, q.device, stream)
+    elif _need(out, torch.float32, "out").shape != q.shape:
+        raise ValueError("out must have q's shape")
+    hi, lo = (_new(q.shape, torch.float16, q.device, stream) if want_split else None for _ in range(2))
+    if workspace is None:
+        nbytes = lib.attn_paged_workspace_size(T, n, Hq, cache.n_kv_heads, mq, mlb)
+        workspace = _new((max(nbytes, 16),), torch.uint8, q.device, stream)
+    cs = cache.struct()
+    _check("attn_paged",
+           lib.attn_paged(_ptr(q), ld, T, Hq, C.byref(cs), _ptr(page_table), page_table.shape[1], n, _ptr(q_start),
+                          _ptr(lens), mq, mlb, float(softmax_scale), _ptr(out), _ptr(hi), _ptr(lo), _ptr(workspace),
+                          workspace.numel() * workspace.element_size(), _stream(stream)))
+    return (out, hi, lo) if want_split else out
+
+
+def softmax_rows(logits, inv_temperature=1.0, out=None, stream=None):
+    """fp32 logits [rows, n] -> probabilities of logits * inv_temperature (out may be logits)."""
+    ld = _rows_of(logits, "logits")
+    _same_device(logits, out)
+    if out is None:
+        out = _new(logits.shape, torch.float32, logits.device, stream)
+    elif out.shape != logits.shape:
+        raise ValueError("out must have the shape of logits")
+    _check("softmax_rows", lib.softmax_rows(_ptr(logits), logits.shape[0], logits.shape[1], ld, float(inv_temperature),
+                                            _ptr(out), _rows_of(out, "out"), _stream(stream)))
+    return out
+
+
+def spec_verify(target, draft, draft_tokens, u_accept, u_sample, n_draft=None, tokens=None, n_accepted=None,
+                stream=None):
+    """Verifies drafted tokens int32 [B, m] against target probabilities fp32 [B, m + 1, V] and draft probabilities
+    fp32 [B, m, V] (or None) with the uniforms u_accept [B, m] and u_sample [B]: tokens int32 [B, m + 1] (accepted,
+    next, then -1) and n_accepted int32 [B]."""
+    _need(target, torch.float32, "target"), _need(draft_tokens, torch.int32, "draft_tokens")
+    _need(u_accept, torch.float32, "u_accept"), _need(u_sample, torch.float32, "u_sample")
+    B, m1, V = target.shape
+    m = m1 - 1
+    if draft_tokens.shape != (B, m) or u_accept.shape != (B, m) or u_sample.shape != (B,):
+        raise ValueError("target [B, m + 1, V], draft_tokens and u_accept [B, m] and u_sample [B] must agree")
+    if draft is not None and _need(draft, torch.float32, "draft").shape != (B, m, V):
+        raise ValueError("draft must be [B, m, V]")
+    if n_draft is not None and _need(n_draft, torch.int32, "n_draft").shape != (B,):
+        raise ValueError("n_draft must be [B]")
+    _same_device(target, draft, draft_tokens, u_accept, u_sample, n_draft, tokens, n_accepted)
+    if tokens is None:
+        tokens = _new((B, m1), torch.int32, target.device, stream)
+    elif _need(tokens, torch.int32, "tokens").shape != (B, m1):
+        raise ValueError("tokens must be [B, m + 1]")
+    if n_accepted is None:
+        n_accepted = _new((B,), torch.int32, target.device, stream)
+    elif _need(n_accepted, torch.int32, "n_accepted").shape != (B,):
+        raise ValueError("n_accepted must be [B]")
+    _check("spec_verify", lib.spec_verify(_ptr(target), V, _ptr(draft), V, B, m, V, _ptr(draft_tokens), _ptr(n_draft),
+                                          _ptr(u_accept), _ptr(u_sample), _ptr(tokens), _ptr(n_accepted),
+                                          _stream(stream)))
+    return tokens, n_accepted
 
 
 def rope_tables(max_pos: int, base: float = 10000.0, device="cuda", stream=None):

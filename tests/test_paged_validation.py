@@ -1,0 +1,108 @@
+"""Host-side argument checks of the paged-cache operators (CPU only): every
+call below returns its status before touching the GPU."""
+import ctypes as C
+
+import pytest
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+PTR = C.c_void_p(0x100000)  # aligned dummy device address
+ODD = C.c_void_p(0x100004)
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def inv():
+    from invariant_numerics_b200 import invnum
+    return invnum
+
+
+def cache(inv, n_pages=10, hkv=8, page=16, d=128, k=PTR.value):
+    return inv.PagedKVCacheStruct(k, PTR.value, PTR.value, PTR.value, n_pages, hkv, page, d)
+
+
+def append(inv, **kw):
+    a = dict(qkv=PTR, ld=48 * 128, T=4, hq=32, c=cache(inv), table=PTR, ld_table=5, n=2, start=PTR, lens=PTR, cos=PTR,
+             sin=PTR, max_pos=100, qg=None, kg=None, eps=1e-6, out=PTR)
+    a.update(kw)
+    c = a["c"]
+    return inv.lib.kv_append_paged(a["qkv"], a["ld"], a["T"], a["hq"], None if c is None else C.byref(c), a["table"],
+                                   a["ld_table"], a["n"], a["start"], a["lens"], a["cos"], a["sin"], a["max_pos"],
+                                   a["qg"], a["kg"], a["eps"], a["out"], None)
+
+
+def attend(inv, **kw):
+    a = dict(q=PTR, ld=32 * 128, T=4, hq=32, c=cache(inv), table=PTR, ld_table=50, n=2, start=PTR, lens=PTR, mq=0,
+             mlb=0, sigma=0.1, out=PTR, hi=None, lo=None, ws=PTR, nb=10 ** 12)
+    a.update(kw)
+    c = a["c"]
+    return inv.lib.attn_paged(a["q"], a["ld"], a["T"], a["hq"], None if c is None else C.byref(c), a["table"],
+                              a["ld_table"], a["n"], a["start"], a["lens"], a["mq"], a["mlb"], a["sigma"], a["out"],
+                              a["hi"], a["lo"], a["ws"], a["nb"], None)
+
+
+@pytest.mark.parametrize("call", [append, attend])
+def test_what_both_refuse(inv, call):
+    assert call(inv, T=0) == OK and call(inv, n=0) == OK
+    assert call(inv, c=None) == INVALID
+    assert call(inv, T=-1) == INVALID and call(inv, n=-1) == INVALID and call(inv, ld_table=-1) == INVALID
+    assert call(inv, hq=0) == INVALID
+    for name in ("table", "start", "lens", "out"):
+        assert call(inv, **{name: None}) == INVALID, name
+    for c, want in ((cache(inv, d=64), UNSUPPORTED), (cache(inv, page=8), UNSUPPORTED), (cache(inv, page=48), UNSUPPORTED),
+                    (cache(inv, page=512), UNSUPPORTED), (cache(inv, n_pages=0), INVALID), (cache(inv, hkv=0), INVALID),
+                    (cache(inv, hkv=5), UNSUPPORTED), (cache(inv, n_pages=1 << 27), UNSUPPORTED),
+                    (cache(inv, k=None), INVALID), (cache(inv, k=ODD.value), INVALID)):
+        assert call(inv, c=c) == want
+
+
+def test_append_refusals(inv):
+    assert append(inv, ld=48 * 128 - 4) == INVALID and append(inv, ld=48 * 128 + 2) == INVALID
+    assert append(inv, qkv=None) == INVALID and append(inv, qkv=ODD) == INVALID
+    assert append(inv, cos=None) == INVALID and append(inv, sin=None) == INVALID and append(inv, max_pos=0) == INVALID
+    assert append(inv, eps=-1e-6) == INVALID and append(inv, eps=NAN) == INVALID
+    for name in ("qg", "kg", "out", "cos"):
+        assert append(inv, **{name: ODD}) == INVALID, name
+
+
+def test_attend_refusals(inv):
+    assert attend(inv, ld=32 * 128 - 4) == INVALID and attend(inv, ld=32 * 128 + 2) == INVALID
+    assert attend(inv, q=None) == INVALID and attend(inv, q=ODD) == INVALID and attend(inv, out=ODD) == INVALID
+    assert attend(inv, hi=PTR) == INVALID and attend(inv, lo=PTR) == INVALID
+    assert attend(inv, hi=ODD, lo=PTR) == INVALID
+    for s in (-0.1, INF, NAN):
+        assert attend(inv, sigma=s) == INVALID
+    assert attend(inv, hq=17 * 8, ld=17 * 8 * 128) == UNSUPPORTED
+    need = inv.lib.attn_paged_workspace_size(4, 2, 32, 8, 4, 800)
+    assert need > 0 and attend(inv, nb=need - 1) == WORKSPACE and attend(inv, ws=ODD) == INVALID
+    assert attend(inv, nb=0) == WORKSPACE and attend(inv, ws=None) == INVALID
+
+
+def test_workspace_size(inv):
+    f = inv.lib.attn_paged_workspace_size
+    for bad in ((0, 2, 32, 8, 4, 800), (4, 0, 32, 8, 4, 800), (4, 2, 0, 8, 4, 800), (4, 2, 32, 0, 4, 800),
+                (4, 2, 32, 8, 4, 0)):
+        assert f(*bad) == 0
+    assert f(4, 2, 32, 8, 4, 8192) >= f(4, 2, 32, 8, 4, 4096) >= f(4, 2, 32, 8, 4, 513)
+
+
+def test_softmax_refusals(inv):
+    f = inv.lib.softmax_rows
+    assert f(PTR, 0, 10, 10, 1.0, PTR, 10, None) == OK
+    assert f(PTR, -1, 10, 10, 1.0, PTR, 10, None) == INVALID
+    assert f(PTR, 2, 0, 10, 1.0, PTR, 10, None) == INVALID
+    assert f(PTR, 2, 10, 9, 1.0, PTR, 10, None) == INVALID and f(PTR, 2, 10, 10, 1.0, PTR, 9, None) == INVALID
+    for t in (0.0, -1.0, INF, NAN):
+        assert f(PTR, 2, 10, 10, t, PTR, 10, None) == INVALID
+    assert f(None, 2, 10, 10, 1.0, PTR, 10, None) == INVALID and f(PTR, 2, 10, 10, 1.0, None, 10, None) == INVALID
+    assert f(PTR, 2, 10, 12, 1.0, PTR, 10, None) == INVALID  # in place with another stride
+
+
+def test_verify_refusals(inv):
+    f = inv.lib.spec_verify
+    ok = [PTR, 100, PTR, 100, 2, 3, 100, PTR, None, PTR, PTR, PTR, PTR]
+    call = lambda **kw: f(*[kw.get(f"a{i}", x) for i, x in enumerate(ok)], None)
+    assert call(a4=0) == OK
+    assert call(a4=-1) == INVALID and call(a5=-1) == INVALID and call(a6=0) == INVALID
+    assert call(a1=99) == INVALID and call(a3=99) == INVALID
+    for i in (0, 7, 9, 10, 11, 12):
+        assert call(**{f"a{i}": None}) == INVALID, i
