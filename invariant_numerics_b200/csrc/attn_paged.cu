@@ -40,6 +40,9 @@ struct AttnArgs {
   inv::PagedView c;
   inv::RaggedBatch rb;
   int max_q, max_len, S_max;
+  int few;          // sequences with at most this many new tokens are the mma.sync kernel's
+  int by_seq;       // partials indexed by (sequence, token < few) instead of by row
+  int segs;         // segments per CTA of the tcgen05 kernel (split over keys)
   float sigma_l2;   // sigma log2 e
   float* part_o;    // [T][Hq][S_max][128]
   float2* part_ml;  // [T][Hq][S_max]
@@ -97,20 +100,22 @@ struct Tile {
   int len, n_new;
 };
 
-// Tiles are numbered so that sequence i owns the ids q_start[i] / per + i ..:
-// ascending in i and never overlapping (floor((a + n) / per) + 1 - floor(a /
-// per) >= ceil(n / per)), without a pass over the batch.  False: no such tile.
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, int lane, Tile& t) {
-  const int i = inv::warp_upper(a.rb.n_seqs, id, lane, [&](int j) { return a.rb.q_start[j] / per + j; });
-  if (i < 0) return false;
+// Partial results of (row, head): index of segment 0.
+__device__ __forceinline__ int64_t part_index(const AttnArgs& a, int seq, int tok, int row, int head) {
+  const int64_t r = a.by_seq ? (int64_t)seq * a.few + tok : row;
+  return (r * a.Hq + head) * a.S_max;
+}
+[[maybe_unused]] __device__ __forceinline__ int64_t part_count(const AttnArgs& a) {
+  return (a.by_seq ? (int64_t)a.rb.n_seqs * a.few : (int64_t)a.T) * a.Hq * a.S_max;
+}
+
+// Checks sequence i's descriptors; fills everything but the tile's tokens.
+__device__ __forceinline__ bool load_seq(const AttnArgs& a, int i, int lane, Tile& t) {
   const int q0 = a.rb.q_start[i], q1 = a.rb.q_start[i + 1];
-  const int tile = id - (q0 / per + i);
   t.seq = i;
+  t.row0 = q0;
   t.n_new = q1 - q0;
-  t.tok0 = tile * per;
-  if (q0 < 0 || q1 > a.T || t.n_new <= 0 || t.tok0 >= t.n_new) return false;
-  t.ntok = min(per, t.n_new - t.tok0);
-  t.row0 = q0 + t.tok0;
+  if (q0 < 0 || q1 > a.T || t.n_new <= 0) return false;
   t.len = a.rb.len[i];
   if (t.n_new > a.max_q || t.len < t.n_new || t.len > a.max_len) {
     if (lane == 0) record_status(a.status, INV_ERR_INVALID_ARG);
@@ -119,10 +124,23 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, in
   return true;
 }
 
+// Tiles are numbered so that sequence i owns the ids q_start[i] / per + i ..:
+// ascending in i and never overlapping (floor((a + n) / per) + 1 - floor(a /
+// per) >= ceil(n / per)), without a pass over the batch.  False: no such tile.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, int lane, Tile& t) {
+  const int i = inv::warp_upper(a.rb.n_seqs, id, lane, [&](int j) { return a.rb.q_start[j] / per + j; });
+  if (i < 0 || !load_seq(a, i, lane, t)) return false;
+  t.tok0 = (id - (t.row0 / per + i)) * per;
+  if (t.tok0 >= t.n_new) return false;
+  t.ntok = min(per, t.n_new - t.tok0);
+  t.row0 += t.tok0;
+  return true;
+}
+
 // ------------------------------------------------------- few rows: mma.sync --
 //
-// One CTA (4 warps) per (tile of up to 8 NT rows, kv head, segment).  A row is
-// a (token, query head of the group) pair.  K and V blocks of 128 keys stream
+// One CTA (4 warps) per (sequence of at most 8 NT rows, kv head, segment).  A
+// row is a (token, query head of the group) pair.  K and V blocks of 128 keys stream
 // through a ring of 32 KB slots (2-D TMA, 128-byte swizzle, one box per page
 // and half of d).  S^T = K Q^T: warp w owns keys 32w .. 32w+31 of the block
 // (rows of two m-tiles), the tile's rows are the MMA columns.  O^T = V^T W:
@@ -160,7 +178,9 @@ __global__ void __launch_bounds__(TH)
   const int seg = blockIdx.x % a.S_max, h = blockIdx.y;
   const int G = a.G, per = (8 * NT) / G, Hkv = a.c.n_kv_heads;
   Tile t;
-  if (!find_tile(a, blockIdx.x / a.S_max, per, lane, t)) return;
+  if (!load_seq(a, blockIdx.x / a.S_max, lane, t) || t.n_new > min(a.few, per)) return;
+  t.tok0 = 0;
+  t.ntok = t.n_new;
   const int pos0 = t.len - t.n_new + t.tok0;           // position of the tile's first token
   const int key0 = seg * SEG, last = pos0 + t.ntok;    // keys of the tile: 0 .. last - 1
   if (key0 >= last) return;
@@ -472,9 +492,8 @@ __global__ void __launch_bounds__(TH)
     for (int i = 0; i < 2; ++i) {
       const int r = 8 * nt + 2 * c + i, tok = r / G;
       if (!ok || nrow[nt][i] <= 0) continue;
-      const int64_t ro = (int64_t)(t.row0 + tok) * a.Hq + h * G + (r - tok * G);
-      const int64_t rs = ro * a.S_max + seg;
-      if (!INV_IN_BOUNDS(a.status, rs, (int64_t)a.T * a.Hq * a.S_max)) continue;
+      const int64_t rs = part_index(a, t.seq, tok, t.row0 + tok, h * G + (r - tok * G)) + seg;
+      if (!INV_IN_BOUNDS(a.status, rs, part_count(a))) continue;
       const float un = inv::pow2f(1 - E[nt][i]);
       float* po = a.part_o + rs * D + 32 * warp + g;
 #pragma unroll
@@ -493,6 +512,577 @@ __global__ void __launch_bounds__(TH)
       inv::mbar_wait(&sm.full[i % NST], (i / NST) & 1, a.wait_ns, nullptr, a.status);
 }
 
+// --------------------------------------------------------- many rows: tcgen05 --
+//
+// One CTA per (tile of 128 rows, kv head, range of segments), 16 warps:
+//   warps 0-7   softmax: thread (row, half).  Reads its 64 of the block's 128
+//               scores from tensor memory, writes w as binary16 hi and lo over
+//               them, and adds the finished block's O (its 64 dims) to the
+//               registers that hold the segment's sum.
+//   warps 8-11  load codes (16 bytes a thread, one operand ahead in registers),
+//               unpack them and store hi and lo as swizzled MMA operands.
+//   warp 13     stores the blocks' scales and the running maximum of V's.
+//   warp 12     issues the MMAs: S = Q K^T (A = Q in tensor memory, B = K in
+//               shared memory, K-major), O = W V (A = W in tensor memory, B =
+//               V, MN-major).  Order S(i+1), O(i): the tensor core forms the
+//               next scores while the softmax of this block runs.
+// Tensor memory (512 columns): Q hi | Q lo (64 each), two score blocks (128
+// each, W in place of the scores), O (128).
+// Each product is three MMAs (hi lo, lo hi, hi hi): 3 x 2 x 128 x 128 x 128
+// multiply-adds a block, 3072 clocks at the tensor core's rate, is the bound.
+constexpr int MANY_ROWS = 128;
+constexpr int SOFT_T = 256, CONV_T = 128;
+constexpr int MANY_T = SOFT_T + CONV_T + 128;
+constexpr int MMA_WARP = (SOFT_T + CONV_T) / 32, SCALE_WARP = MMA_WARP + 1;
+// Registers a thread: the CTA starts with MANY_REGS for everyone (launch_many
+// checks it), each role then takes or returns some; the sum stays the same.
+constexpr int MANY_REGS = 128, SOFT_REGS = 160, CONV_REGS = 136, REST_REGS = 56;
+static_assert(SOFT_T * SOFT_REGS + CONV_T * CONV_REGS + 128 * REST_REGS <= MANY_T * MANY_REGS, "registers of the CTA");
+constexpr int OPER = BLK * D * 2;  // bytes of one binary16 operand (hi or lo) of a block
+constexpr uint32_t COL_QH = 0, COL_QL = 64, COL_S = 128, COL_O = 384;
+
+struct __align__(1024) ManySmem {
+  uint8_t k[2 * OPER];  // hi, lo; [d half][key][64], 128-byte swizzle
+  uint8_t v[2 * OPER];
+  float o_sum[64 * SOFT_T];  // kDirect: sum over the folded segments, [dim][thread]
+  // scales of the last 4 blocks: K; V; V 2^E with the whole block's E; running maximum of V in the segment
+  float ks[4][BLK], vs[4][BLK], vs2[4][BLK], pm[4][BLK];
+  float2 red[2][2][MANY_ROWS];  // [block parity][half][row]: maximum, and l of the segment that ended
+  uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], o_full, o_empty, sc_full[4], sc_empty[4], pair[4], done;
+  uint32_t tmem;
+  int abort;
+};
+constexpr size_t kManySmem = sizeof(ManySmem) + 1024;
+static_assert(kManySmem <= 227 * 1024, "shared memory of one SM");
+
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: 8 rows of K x 64 elements are 1024 bytes
+// (stride SBO between them along K), 64-element groups of N are LBO apart.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(sbo >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// 32 lanes x 32 consecutive columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+      "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Splits two values into binary16 hi and lo pairs (split_plain of each).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+[[maybe_unused]] __device__ __forceinline__ int64_t cache_rows(const AttnArgs& a) {
+  return ((int64_t)a.c.n_pages * a.c.n_kv_heads) << a.c.page_shift;
+}
+
+// Row of a cached key in the pages of sequence seq, kv head h; -1 behind the
+// last key and for a page outside the cache.
+__device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int seq, int h, int key, int last) {
+  if (key >= last) return -1;
+  const int sh = a.c.page_shift, pg = a.rb.page_table[seq * a.rb.ld_table + (key >> sh)];
+  if (pg < 0 || pg >= a.c.n_pages) {
+    record_status(a.status, INV_ERR_INVALID_ARG);
+    return -1;
+  }
+  return (((int64_t)pg * a.c.n_kv_heads + h) << sh) + (key & ((1 << sh) - 1));
+}
+
+// The whole warp waits; false once any wait of the CTA gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, const AttnArgs& a, int* abort) {
+  bool ok = true;
+  if (lane == 0) ok = inv::mbar_wait(bar, parity, a.wait_ns, abort, a.status);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <bool kDirect>
+__global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_constant__ AttnArgs a) {
+  inv::grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.G, per = MANY_ROWS / G, h = blockIdx.y;
+  Tile t;
+  // the last tiles of a prompt see the most keys: they start first
+  if (!find_tile(a, gridDim.x - 1 - blockIdx.x, per, lane, t) || t.n_new <= a.few) return;
+  const int pos0 = t.len - t.n_new + t.tok0, last = pos0 + t.ntok;
+  const int b0 = blockIdx.z * a.segs * (SEG / BLK);
+  const int b1 = min((last + BLK - 1) / BLK, b0 + a.segs * (SEG / BLK));
+  const int n = b1 - b0;
+  if (n <= 0) return;
+
+  extern __shared__ uint8_t smem_raw[];
+  ManySmem& sm = *reinterpret_cast<ManySmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (tid == 0) {
+    inv::mbar_init(&sm.q_full, SOFT_T);
+    inv::mbar_init(&sm.k_full, CONV_T);
+    inv::mbar_init(&sm.v_full, CONV_T);
+    inv::mbar_init(&sm.k_empty, 1);
+    inv::mbar_init(&sm.v_empty, 1);
+    inv::mbar_init(&sm.o_full, 1);
+    inv::mbar_init(&sm.o_empty, SOFT_T);
+    inv::mbar_init(&sm.done, 1);
+    for (int i = 0; i < 2; ++i) {
+      inv::mbar_init(&sm.s_full[i], 1);
+      inv::mbar_init(&sm.p_full[i], SOFT_T);
+    }
+    for (int i = 0; i < 4; ++i) {
+      inv::mbar_init(&sm.sc_full[i], 32);
+      inv::mbar_init(&sm.sc_empty[i], SOFT_T);
+      inv::mbar_init(&sm.pair[i], 64);
+    }
+    sm.abort = 0;
+    inv::fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    inv::tmem_alloc(&sm.tmem, 512);
+    inv::tmem_relinquish();
+  }
+  inv::tc_fence_before();
+  __syncthreads();
+  inv::tc_fence_after();
+  const uint32_t tm = sm.tmem;
+  bool ok = true;
+
+  if (warp < SOFT_T / 32) {
+    // ================================================================ softmax
+    regs_inc<SOFT_REGS>();
+    const int hf = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int tok = r / G, head = h * G + (r - tok * G);
+    const bool valid = tok < t.ntok && tok < per;
+    const int nrow = valid ? pos0 + tok + 1 : 0;  // keys the row sees
+    const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21);
+    float kap;
+    {
+      float4 x[16];
+      float m = 0.0f;
+      const int64_t iq = (int64_t)(t.row0 + tok) * a.ld_q + (int64_t)head * D + hf * 64;
+      const bool in = valid && INV_SPAN_IN_BOUNDS(a.status, iq, iq + 63, (int64_t)(a.T - 1) * a.ld_q + (int64_t)a.Hq * D);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[j] = in ? reinterpret_cast<const float4*>(a.q + iq)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
+      }
+      sm.red[0][hf][r].x = m;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      m = fmaxf(m, sm.red[0][hf ^ 1][r].x);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int e = inv::norm_exp(m);
+      const float f = inv::pow2f(e);
+      kap = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 y = x[8 * c + j];
+          split2(__fmul_rn(y.x, f), __fmul_rn(y.y, f), hi[2 * j], lo[2 * j]);
+          split2(__fmul_rn(y.z, f), __fmul_rn(y.w, f), hi[2 * j + 1], lo[2 * j + 1]);
+        }
+        tmem_st16(lanes + COL_QH + hf * 32 + c * 16, hi);
+        tmem_st16(lanes + COL_QL + hf * 32 + c * 16, lo);
+      }
+      tmem_wait_st();
+      inv::tc_fence_before();
+      inv::mbar_arrive(&sm.q_full);
+    }
+
+    float O[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) O[j] = 0.0f;
+    float M = -INFINITY, mk = -INFINITY, L0 = 0.0f, L1 = 0.0f;
+    int E = 0;
+    float Mt = -INFINITY, Lt = 0.0f;                 // kDirect: folded segments
+    float beta = 0.0f;                               // of the block whose O is still to be added
+    bool add = false, ends = false;                  // it has keys of this row; it ends a segment
+    float mk_s = 0.0f, l_s = 0.0f;                   // the ended segment's m and l
+    int E_s = 0;
+    uint32_t exch = 0;                               // pair exchanges so far
+
+    // adds block j's O to the sum; at a segment's end passes the segment on
+    const auto fold = [&](int j) {
+      ok = warp_wait(&sm.o_full, j & 1, lane, a, &sm.abort) && ok;
+      inv::tc_fence_after();
+      if (__any_sync(0xffffffffu, add)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld32(lanes + COL_O + hf * 64 + c * 32, v);
+          inv::tmem_wait_ld();
+          if (add) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) O[c * 32 + i] = __fmaf_rn(O[c * 32 + i], beta, __uint_as_float(v[i]));
+          }
+        }
+      }
+      inv::tc_fence_before();
+      inv::mbar_arrive(&sm.o_empty);
+      if (!ends) return;
+      const int seg = (b0 + j) / (SEG / BLK);
+      if (ok && nrow > seg * SEG) {
+        const float un = inv::pow2f(1 - E_s);
+        if constexpr (kDirect) {
+          const float Mn = fmaxf(Mt, mk_s);
+          const float fa = seg == 0 ? 0.0f : inv::ex2(__fsub_rn(Mt, Mn)), fb = inv::ex2(__fsub_rn(mk_s, Mn));
+          Mt = Mn;
+          Lt = __fmaf_rn(Lt, fa, __fmul_rn(l_s, fb));
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            float* p = sm.o_sum + i * SOFT_T + tid;
+            *p = __fmaf_rn(seg == 0 ? 0.0f : *p, fa, __fmul_rn(__fmul_rn(O[i], un), fb));
+          }
+        } else {
+          const int64_t rs = part_index(a, t.seq, t.tok0 + tok, t.row0 + tok, head) + seg;
+          if (INV_IN_BOUNDS(a.status, rs, part_count(a))) {
+            float4* po = reinterpret_cast<float4*>(a.part_o + rs * D + hf * 64);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              po[i] = make_float4(__fmul_rn(O[4 * i], un), __fmul_rn(O[4 * i + 1], un), __fmul_rn(O[4 * i + 2], un),
+                                  __fmul_rn(O[4 * i + 3], un));
+            if (hf == 0) a.part_ml[rs] = make_float2(mk_s, l_s);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 64; ++i) O[i] = 0.0f;
+    };
+    // exchanges (maximum, l) with the thread of the row's other half
+    const auto exchange = [&](float2 mine) {
+      sm.red[exch & 1][hf][r] = mine;
+      inv::mbar_arrive(&sm.pair[warp & 3]);
+      ok = warp_wait(&sm.pair[warp & 3], exch & 1, lane, a, &sm.abort) && ok;
+      const float2 other = sm.red[exch & 1][hf ^ 1][r];
+      ++exch;
+      return other;
+    };
+
+    for (int i = 0; i < n && ok; ++i) {
+      const int b = b0 + i, sl = i & 3;
+      const bool first = (b & (SEG / BLK - 1)) == 0;
+      const uint32_t sc = lanes + COL_S + (i & 1) * 128 + hf * 64;
+      const int nv = min(BLK, nrow - b * BLK) - hf * 64;  // visible keys among this thread's 64 (may be <= 0 or > 64)
+      const bool row_on = nrow > b * BLK;
+      const bool any = __any_sync(0xffffffffu, row_on), full = __all_sync(0xffffffffu, nrow >= (b + 1) * BLK);
+      ok = warp_wait(&sm.sc_full[sl], (i >> 2) & 1, lane, a, &sm.abort) && ok;
+      ok = warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, lane, a, &sm.abort) && ok;
+      inv::tc_fence_after();
+      float mx = -INFINITY;
+      if (any) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld32(sc + c * 32, v);
+          inv::tmem_wait_ld();
+          const float* ks = sm.ks[sl] + hf * 64 + c * 32;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = __fmul_rn(__uint_as_float(v[j]), ks[j]);
+            mx = fmaxf(mx, full || c * 32 + j < nv ? x : -INFINITY);
+          }
+        }
+      }
+      const bool starts = first && i > 0;
+      const float mk_old = mk;
+      const int E_old = E;
+      const bool add_old = add, ends_old = starts;
+      const float beta_old = beta;
+      if (any || starts) {
+        const float lh = __fadd_rn(L0, L1);
+        const float2 other = exchange(make_float2(mx, lh));
+        mx = fmaxf(mx, other.x);
+        if (starts) {
+          mk_s = mk;
+          E_s = E;
+          l_s = hf == 0 ? __fadd_rn(lh, other.y) : __fadd_rn(other.y, lh);
+        }
+      }
+      if (first) {
+        M = -INFINITY;
+        L0 = L1 = 0.0f;
+      }
+      add = row_on;
+      beta = 1.0f;
+      if (row_on) {
+        M = fmaxf(M, mx);
+        mk = __fmul_rn(M, kap);
+        E = inv::norm_exp(sm.pm[sl][min(BLK, nrow - b * BLK) - 1]);
+        const float alpha = first ? 0.0f : inv::ex2(__fsub_rn(mk_old, mk));
+        beta = first ? 0.0f : __fmul_rn(alpha, inv::pow2f(max(E - E_old, -126)));
+        L0 = __fmul_rn(L0, alpha);
+        L1 = __fmul_rn(L1, alpha);
+      }
+      if (any) {
+        const float vscale = inv::pow2f(E);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld32(sc + c * 32, v);
+          inv::tmem_wait_ld();
+          const float* ks = sm.ks[sl] + hf * 64 + c * 32;
+          const float* vs = (full ? sm.vs2[sl] : sm.vs[sl]) + hf * 64 + c * 32;
+          float s[8];
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float p[2], w[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              p[u] = 0.0f;
+              w[u] = 0.0f;
+              if (full || c * 32 + j + u < nv) {
+                p[u] = inv::ex2(__fmaf_rn(__fmul_rn(__uint_as_float(v[j + u]), ks[j + u]), kap, -mk));
+                w[u] = __fmul_rn(p[u], full ? vs[j + u] : __fmul_rn(vs[j + u], vscale));
+              }
+              s[(j + u) & 7] = j + u < 8 ? p[u] : __fadd_rn(s[(j + u) & 7], p[u]);
+            }
+            split2(w[0], w[1], hi[j >> 1], lo[j >> 1]);
+          }
+          const float g = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])),
+                                    __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
+          if (c == 0)
+            L0 = __fadd_rn(L0, g);
+          else
+            L1 = __fadd_rn(L1, g);
+          tmem_st16(sc + c * 32, hi);
+          tmem_st16(sc + c * 32 + 16, lo);
+        }
+        tmem_wait_st();
+      }
+      inv::tc_fence_before();
+      inv::mbar_arrive(&sm.p_full[i & 1]);
+      inv::mbar_arrive(&sm.sc_empty[sl]);
+      if (i > 0) {  // the previous block's O, formed during this softmax
+        const float beta_new = beta;
+        const bool add_new = add;
+        beta = beta_old;
+        add = add_old;
+        ends = ends_old;
+        fold(i - 1);
+        beta = beta_new;
+        add = add_new;
+      }
+    }
+    if (ok) {
+      const float lh = __fadd_rn(L0, L1);
+      const float2 other = exchange(make_float2(0.0f, lh));
+      mk_s = mk;
+      E_s = E;
+      l_s = hf == 0 ? __fadd_rn(lh, other.y) : __fadd_rn(other.y, lh);
+      ends = true;
+      fold(n - 1);
+      if constexpr (kDirect) {
+        if (ok && nrow > 0) {
+          const float il = __frcp_rn(Lt);
+          const int64_t io = ((int64_t)(t.row0 + tok) * a.Hq + head) * D + hf * 64;
+          if (INV_SPAN_IN_BOUNDS(a.status, io, io + 63, (int64_t)a.T * a.Hq * D)) {
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              const float* p = sm.o_sum + i * SOFT_T + tid;
+              store_out4(a, io + i, make_float4(__fmul_rn(p[0], il), __fmul_rn(p[SOFT_T], il),
+                                                __fmul_rn(p[2 * SOFT_T], il), __fmul_rn(p[3 * SOFT_T], il)));
+            }
+          }
+        }
+      }
+    }
+  } else if (warp < MMA_WARP) {
+    // ============================================================= converters
+    regs_inc<CONV_REGS>();
+    const int ct = tid - SOFT_T, kr = ct >> 4, ch = ct & 15;  // key kr of every 8, dims 8 ch .. 8 ch + 7
+    // half an operand (64 keys from kh on) of block i into registers
+    const auto load = [&](const int16_t* codes, int i, int kh, uint4 (&x)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t row = cache_row(a, t.seq, h, (b0 + i) * BLK + kh + 8 * j + kr, last);
+        const bool in = row >= 0 && INV_IN_BOUNDS(a.status, row, cache_rows(a));
+        x[j] = in ? __ldg(reinterpret_cast<const uint4*>(codes + row * D) + ch) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    const auto store = [&](uint8_t* dst, int kh, const uint4 (&x)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = kh + 8 * j + kr;
+        uint4 hi, lo;
+        inv::unpack_code(x[j].x, hi.x, lo.x);
+        inv::unpack_code(x[j].y, hi.y, lo.y);
+        inv::unpack_code(x[j].z, hi.z, lo.z);
+        inv::unpack_code(x[j].w, hi.w, lo.w);
+        uint8_t* p = dst + (ch >> 3) * (BLK * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+        *reinterpret_cast<uint4*>(p) = hi;
+        *reinterpret_cast<uint4*>(p + OPER) = lo;
+      }
+    };
+    // Operands in the order they can be stored: K 0, then K i+1 (free once S(i) is formed) before V i (free once
+    // O(i-1) is formed).  Operand s: K of block i or V of block i.
+    const auto operand = [&](int s, bool& is_v) {
+      is_v = s > 0 && (!(s & 1) || s == 2 * n - 1);
+      return s == 0 ? 0 : (s & 1) ? (s == 2 * n - 1 ? n - 1 : (s + 1) / 2) : s / 2 - 1;
+    };
+    uint4 xa[8], xb[8];
+    load(a.c.k, 0, 0, xa);
+    load(a.c.k, 0, 64, xb);
+    for (int s = 0; s < 2 * n && ok; ++s) {
+      bool is_v, next_v = false;
+      const int i = operand(s, is_v), ni = s + 1 < 2 * n ? operand(s + 1, next_v) : 0;
+      const int16_t* next = next_v ? a.c.v : a.c.k;
+      if (i > 0) ok = warp_wait(is_v ? &sm.v_empty : &sm.k_empty, (i - 1) & 1, lane, a, &sm.abort) && ok;
+      uint8_t* dst = is_v ? sm.v : sm.k;
+      store(dst, 0, xa);
+      if (s + 1 < 2 * n) load(next, ni, 0, xa);
+      store(dst, 64, xb);
+      if (s + 1 < 2 * n) load(next, ni, 64, xb);
+      inv::fence_proxy_async_smem();
+      inv::mbar_arrive(is_v ? &sm.v_full : &sm.k_full);
+    }
+  } else {
+    regs_dec<REST_REGS>();
+    if (warp == SCALE_WARP) {
+    // ================================================================= scales
+    float carry = 0.0f;  // largest V scale of the segment so far
+    for (int i = 0; i < n && ok; ++i) {
+      // keys 4 lane .. 4 lane + 3 of the block (one page)
+      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+      const int key = (b0 + i) * BLK + 4 * lane, sl = i & 3;
+      const int64_t row = cache_row(a, t.seq, h, key, last);
+      if (row >= 0 && INV_SPAN_IN_BOUNDS(a.status, row, row + 3, cache_rows(a))) {
+        kv = *reinterpret_cast<const float4*>(a.c.k_scale + row);
+        vv = *reinterpret_cast<const float4*>(a.c.v_scale + row);
+        if (key + 1 >= last) kv.y = vv.y = 0.0f;
+        if (key + 2 >= last) kv.z = vv.z = 0.0f;
+        if (key + 3 >= last) kv.w = vv.w = 0.0f;
+      }
+      if (((b0 + i) & (SEG / BLK - 1)) == 0) carry = 0.0f;
+      float4 pv;
+      pv.x = vv.x;
+      pv.y = fmaxf(pv.x, vv.y);
+      pv.z = fmaxf(pv.y, vv.z);
+      pv.w = fmaxf(pv.z, vv.w);
+      float up = pv.w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up = fmaxf(up, x);
+      }
+      float before = __shfl_up_sync(0xffffffffu, up, 1);
+      before = fmaxf(lane == 0 ? 0.0f : before, carry);
+      carry = fmaxf(carry, __shfl_sync(0xffffffffu, up, 31));
+      const float f = inv::pow2f(inv::norm_exp(carry));
+      if (i >= 4) ok = warp_wait(&sm.sc_empty[sl], ((i - 4) >> 2) & 1, lane, a, &sm.abort) && ok;
+      reinterpret_cast<float4*>(sm.ks[sl])[lane] = kv;
+      reinterpret_cast<float4*>(sm.vs[sl])[lane] = vv;
+      reinterpret_cast<float4*>(sm.vs2[sl])[lane] =
+          make_float4(__fmul_rn(vv.x, f), __fmul_rn(vv.y, f), __fmul_rn(vv.z, f), __fmul_rn(vv.w, f));
+      reinterpret_cast<float4*>(sm.pm[sl])[lane] =
+          make_float4(fmaxf(pv.x, before), fmaxf(pv.y, before), fmaxf(pv.z, before), fmaxf(pv.w, before));
+      inv::mbar_arrive(&sm.sc_full[sl]);
+    }
+    } else if (warp == MMA_WARP && lane == 0) {
+    // ==================================================================== MMA
+    constexpr uint32_t ID_S = inv::idesc_f16_f32(MANY_ROWS, BLK);
+    constexpr uint32_t ID_O = inv::idesc_f16_f32(MANY_ROWS, D) | (1u << 16);  // B is MN-major
+    const uint32_t kb = inv::smem_u32(sm.k), vb = inv::smem_u32(sm.v);
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && inv::mbar_wait(bar, parity, a.wait_ns, &sm.abort, a.status);
+    };
+    const auto scores = [&](int i) {
+      wait(&sm.k_full, i & 1);
+      if (!ok) return;
+      inv::tc_fence_after();
+      const uint32_t d = tm + COL_S + (i & 1) * 128;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t off = (k >> 2) * (BLK * 128) + (k & 3) * 32;
+        umma_ts(d, tm + COL_QH + 8 * k, inv::sw128_kmajor_desc(kb + OPER + off), ID_S, k != 0);
+        umma_ts(d, tm + COL_QL + 8 * k, inv::sw128_kmajor_desc(kb + off), ID_S, 1);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_ts(d, tm + COL_QH + 8 * k, inv::sw128_kmajor_desc(kb + (k >> 2) * (BLK * 128) + (k & 3) * 32), ID_S, 1);
+      inv::umma_commit(&sm.k_empty);
+      inv::umma_commit(&sm.s_full[i & 1]);
+    };
+    const auto values = [&](int i) {
+      wait(&sm.p_full[i & 1], (i >> 1) & 1);
+      wait(&sm.v_full, i & 1);
+      if (i > 0) wait(&sm.o_empty, (i - 1) & 1);
+      if (!ok) return;
+      inv::tc_fence_after();
+      const uint32_t w0 = tm + COL_S + (i & 1) * 128, d = tm + COL_O;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t w = w0 + (k >> 1) * 32 + (k & 1) * 8;  // hi; lo 16 columns on
+        umma_ts(d, w, sw128_mnmajor_desc(vb + OPER + k * 2048, BLK * 128, 1024), ID_O, k != 0);
+        umma_ts(d, w + 16, sw128_mnmajor_desc(vb + k * 2048, BLK * 128, 1024), ID_O, 1);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_ts(d, w0 + (k >> 1) * 32 + (k & 1) * 8, sw128_mnmajor_desc(vb + k * 2048, BLK * 128, 1024), ID_O, 1);
+      inv::umma_commit(&sm.v_empty);
+      inv::umma_commit(&sm.o_full);
+    };
+    wait(&sm.q_full, 0);
+    scores(0);
+    for (int i = 1; i < n && ok; ++i) {
+      scores(i);
+      values(i - 1);
+    }
+    if (ok) values(n - 1);
+    // every MMA has finished before tensor memory is given back
+    inv::umma_commit(&sm.done);
+    inv::mbar_wait(&sm.done, 0, a.wait_ns, nullptr, a.status);
+    }
+  }
+  __syncwarp();
+  inv::tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    inv::tc_fence_after();
+    inv::tmem_dealloc(tm, 512);
+  }
+}
+
 // One warp per (row, head): folds the segments in ascending order.
 __global__ void __launch_bounds__(256) attn_fold_kernel(const __grid_constant__ AttnArgs a) {
   inv::grid_wait_prerequisites();
@@ -502,13 +1092,12 @@ __global__ void __launch_bounds__(256) attn_fold_kernel(const __grid_constant__ 
   const int r = (int)(wid / a.Hq);
   const int i = inv::warp_upper(a.rb.n_seqs, r, lane, [&](int j) { return a.rb.q_start[j]; });
   if (i < 0) return;
-  const int q0 = a.rb.q_start[i], q1 = a.rb.q_start[i + 1];
-  if (r >= q1 || q0 < 0 || q1 > a.T) return;
-  const int n_new = q1 - q0, len = a.rb.len[i];
-  if (n_new > a.max_q || len < n_new || len > a.max_len) return;
-  const int n = len - (q1 - r) + 1, S = (n + SEG - 1) / SEG;
-  const int64_t rs = wid * a.S_max;
-  if (!INV_SPAN_IN_BOUNDS(a.status, rs, rs + S - 1, (int64_t)a.T * a.Hq * a.S_max)) return;
+  Tile t;
+  if (!load_seq(a, i, lane, t) || r >= t.row0 + t.n_new) return;
+  if (a.by_seq && t.n_new > a.few) return;  // its rows are finished already
+  const int n = t.len - t.n_new + (r - t.row0) + 1, S = (n + SEG - 1) / SEG;
+  const int64_t rs = part_index(a, i, r - t.row0, r, (int)(wid - (int64_t)r * a.Hq));
+  if (!INV_SPAN_IN_BOUNDS(a.status, rs, rs + S - 1, part_count(a))) return;
   const float4* po = reinterpret_cast<const float4*>(a.part_o + rs * D) + lane;
   float M = -INFINITY, L = 0.0f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -544,16 +1133,59 @@ int allow_smem(F kernel, size_t bytes, bool (&done)[64]) {
 
 int segments(int max_len) { return (max_len + SEG - 1) / SEG; }
 
+// Sequences with at most this many new tokens (32 rows) take the mma.sync kernel.
+int few_tokens(int G) { return 32 / G; }
+int64_t many_tiles(int T, int n_seqs, int G) { return (int64_t)T / (MANY_ROWS / G) + n_seqs; }
+
+// How a call's work is cut: by its sizes and bounds only, and without any
+// effect on the bits.
+struct Plan {
+  bool many;       // some sequence may have more than few_tokens new tokens
+  bool direct;     // the tcgen05 kernel folds all segments of a tile itself
+  int segs;        // else: segments per CTA
+  int64_t parts;   // (row, head) pairs with partial results
+};
+Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
+  const int G = Hq / Hkv, S = segments(max_len), few = few_tokens(G);
+  Plan p = {max_q > few, false, 1, (int64_t)T * Hq};
+  if (!p.many) return p;
+  const int64_t ctas = ((int64_t)T / (MANY_ROWS / G) + 1) * Hkv;
+  p.direct = ctas >= 2 * inv::sm_count() || S == 1;
+  if (p.direct) {
+    p.segs = S;
+    p.parts = (int64_t)n_seqs * few * Hq;
+  }
+  return p;
+}
+
 template <int NT, int NST>
 int launch_few(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   static bool done[64] = {};
   constexpr size_t smem = sizeof(FewSmem<NT, NST>) + 1024;
   const int rc = allow_smem(attn_few_kernel<NT, NST>, smem, done);
   if (rc != INV_OK) return rc;
-  const int per = 8 * NT / a.G;
-  const int64_t tiles = (int64_t)a.T / per + a.rb.n_seqs;
-  if (tiles * a.S_max > 0x7fffffff) return INV_ERR_UNSUPPORTED_SHAPE;
-  attn_few_kernel<NT, NST><<<dim3((unsigned)(tiles * a.S_max), a.c.n_kv_heads), TH, smem, s>>>(tk, tv, a);
+  attn_few_kernel<NT, NST><<<dim3((unsigned)(a.rb.n_seqs * a.S_max), a.c.n_kv_heads), TH, smem, s>>>(tk, tv, a);
+  INV_CHECK_LAUNCH();
+  return INV_OK;
+}
+
+template <bool kDirect>
+int launch_many(const AttnArgs& a, cudaStream_t s) {
+  static bool done[64] = {};
+  static int regs[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return INV_ERR_CUDA;
+  const int rc = allow_smem(attn_many_kernel<kDirect>, kManySmem, done);
+  if (rc != INV_OK) return rc;
+  if (regs[dev] == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, attn_many_kernel<kDirect>) != cudaSuccess) return INV_ERR_CUDA;
+    regs[dev] = fa.numRegs;
+  }
+  // the roles' shares add up to what the CTA starts with; with less, a role would wait for registers for good
+  if (regs[dev] != MANY_REGS) return INV_ERR_CUDA;
+  const dim3 grid((unsigned)many_tiles(a.T, a.rb.n_seqs, a.G), a.c.n_kv_heads, (a.S_max + a.segs - 1) / a.segs);
+  attn_many_kernel<kDirect><<<grid, MANY_T, kManySmem, s>>>(a);
   INV_CHECK_LAUNCH();
   return INV_OK;
 }
@@ -580,8 +1212,10 @@ extern "C" {
 
 size_t attn_paged_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads, int max_q_bound, int max_len_bound) {
   if (T <= 0 || n_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || max_len_bound <= 0) return 0;
-  (void)max_q_bound;
-  return (size_t)T * n_heads * segments(max_len_bound) * (D * sizeof(float) + sizeof(float2));
+  if (n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 16) return 0;
+  const Plan p = make_plan(T, n_seqs, n_heads, n_kv_heads, max_q_bound > 0 && max_q_bound < T ? max_q_bound : T,
+                           max_len_bound);
+  return (size_t)p.parts * segments(max_len_bound) * (D * sizeof(float) + sizeof(float2));
 }
 
 int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged_kv_cache* cache,
@@ -619,29 +1253,35 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   a.rb = {page_table, ld_table, n_seqs, q_start, len};
   a.sigma_l2 = (float)((double)softmax_scale * 1.4426950408889634);
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)T * n_heads * a.S_max * D);
+  const Plan p = make_plan(T, n_seqs, n_heads, cache->n_kv_heads, a.max_q, a.max_len);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.parts * a.S_max * D);
+  a.few = few_tokens(G);
+  a.by_seq = p.many && p.direct;
+  a.segs = p.segs;
+  if ((int64_t)n_seqs * a.S_max > 0x7fffffff || many_tiles(T, n_seqs, G) > 0x7fffffff) return INV_ERR_UNSUPPORTED_SHAPE;
   a.out = out;
   a.out_hi = reinterpret_cast<__half*>(out_hi);
   a.out_lo = reinterpret_cast<__half*>(out_lo);
   a.status = inv::status_ptr();
   a.wait_ns = inv::wait_limit_ns();
-  const uint64_t rows = (uint64_t)cache->n_pages * cache->n_kv_heads * cache->page_size;
+  const uint64_t cache_rows = (uint64_t)cache->n_pages * cache->n_kv_heads * cache->page_size;
   const uint32_t box = cache->page_size < BLK ? cache->page_size : BLK;
   CUtensorMap tk, tv;
-  rc = inv::make_tensor_map_2d(&tk, cache->k, CU_TENSOR_MAP_DATA_TYPE_UINT16, D, rows, 2 * D, 64, box,
+  rc = inv::make_tensor_map_2d(&tk, cache->k, CU_TENSOR_MAP_DATA_TYPE_UINT16, D, cache_rows, 2 * D, 64, box,
                                CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != INV_OK) return rc;
-  rc = inv::make_tensor_map_2d(&tv, cache->v, CU_TENSOR_MAP_DATA_TYPE_UINT16, D, rows, 2 * D, 64, box,
+  rc = inv::make_tensor_map_2d(&tv, cache->v, CU_TENSOR_MAP_DATA_TYPE_UINT16, D, cache_rows, 2 * D, 64, box,
                                CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != INV_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int rows_tile = a.max_q * G;
-  if (rows_tile <= 8)
+  const int rows = (a.max_q < a.few ? a.max_q : a.few) * G;
+  if (rows <= 8)
     rc = launch_few<1, 3>(a, tk, tv, s);
-  else if (rows_tile <= 16)
+  else if (rows <= 16)
     rc = launch_few<2, 3>(a, tk, tv, s);
   else
     rc = launch_few<4, 3>(a, tk, tv, s);
+  if (rc == INV_OK && p.many) rc = p.direct ? launch_many<true>(a, s) : launch_many<false>(a, s);
   if (rc != INV_OK) return rc;
   return launch_fold(a, s);
 }

@@ -126,6 +126,7 @@ ATTEND = [
     ([400], [333], 16, 4, 128),
     ([129, 600], [129, 70], 3, 3, 64),
     ([1111], [600], 20, 2, 16),
+    ([1700, 900, 40, 77], [1200, 900, 1, 5], 32, 8, 64),
 ]
 
 
@@ -172,6 +173,25 @@ def test_attn_paged_rows_do_not_depend_on_the_batch(inv, hq, hkv, page):
         got = inv.attn_paged(q[:n - first], other, t2, i32([0, n - first]), i32([n]), SCALE)
         assert torch.equal(got, full[:n - first])
     assert status() == inv.INV_OK
+
+
+def test_attn_paged_large_batch_equals_its_parts(inv):
+    """A call whose tiles fill the GPU (each tile folds its own segments) against calls of few rows and of one tile
+    (segments joined by another kernel): the same bits."""
+    lens, news, hq, hkv, page = [1500, 1203, 30, 1100], [1500, 900, 1, 6], 32, 8, 32
+    n_pages, table, start, ln = batch(lens, news, page, seed=51)
+    cache = pool(inv, n_pages, hkv, page, seed=52)
+    q = torch.randn(int(start[-1]), hq, 128, generator=gen(53), device="cuda")
+    full = inv.attn_paged(q, cache, table, start, ln, SCALE)
+    st = start.tolist()
+    for i, first, count in ((0, 0, 1), (0, 1499, 1), (0, 700, 7), (0, 511, 2), (0, 1024, 33), (1, 0, 20), (1, 899, 1),
+                            (1, 300, 300), (2, 0, 1), (3, 0, 6), (3, 3, 2)):
+        a = st[i] + first
+        n = lens[i] - news[i] + first + count
+        got = inv.attn_paged(q[a:a + count], cache, table[i:i + 1], i32([0, count]), i32([n]), SCALE)
+        assert torch.equal(got, full[a:a + count]), (i, first, count)
+    again = inv.attn_paged(q, cache, table, start, ln, SCALE)
+    assert torch.equal(again, full) and status() == inv.INV_OK
 
 
 def test_attn_paged_unused_memory_does_not_matter(inv):
