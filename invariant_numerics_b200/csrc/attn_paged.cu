@@ -514,41 +514,49 @@ __global__ void __launch_bounds__(TH)
 
 // --------------------------------------------------------- many rows: tcgen05 --
 //
-// One CTA per (tile of 128 rows, kv head, range of segments), 16 warps:
+// One CTA per (tile of 128 rows, kv head, range of segments), 20 warps:
 //   warps 0-7   softmax: thread (row, half).  Reads its 64 of the block's 128
 //               scores from tensor memory, writes w as binary16 hi and lo over
 //               them, and adds the finished block's O (its 64 dims) to the
 //               registers that hold the segment's sum.
-//   warps 8-11  load codes (16 bytes a thread, one operand ahead in registers),
+//   warps 8-15  load codes (16 bytes a thread, one operand ahead in registers),
 //               unpack them and store hi and lo as swizzled MMA operands.
-//   warp 13     stores the blocks' scales and the running maximum of V's.
-//   warp 12     issues the MMAs: S = Q K^T (A = Q in tensor memory, B = K in
+//   warp 16     issues the MMAs: S = Q K^T (A = Q in tensor memory, B = K in
 //               shared memory, K-major), O = W V (A = W in tensor memory, B =
 //               V, MN-major).  Order S(i+1), O(i): the tensor core forms the
 //               next scores while the softmax of this block runs.
+//   warp 17     stores the blocks' scales, the running maximum of V's, and the
+//               page numbers the converters need.
 // Tensor memory (512 columns): Q hi | Q lo (64 each), two score blocks (128
 // each, W in place of the scores), O (128).
 // Each product is three MMAs (hi lo, lo hi, hi hi): 3 x 2 x 128 x 128 x 128
 // multiply-adds a block, 3072 clocks at the tensor core's rate, is the bound.
+// The roles' loops are kept rolled and each step is written once: unrolled and
+// inlined twice they were 34 KB of instructions a block, more than the SM's
+// instruction cache holds, and every step ran four times slower.
 constexpr int MANY_ROWS = 128;
-constexpr int SOFT_T = 256, CONV_T = 128;
+constexpr int SOFT_T = 256, CONV_T = 256;
 constexpr int MANY_T = SOFT_T + CONV_T + 128;
 constexpr int MMA_WARP = (SOFT_T + CONV_T) / 32, SCALE_WARP = MMA_WARP + 1;
 // Registers a thread: the CTA starts with MANY_REGS for everyone (launch_many
 // checks it), each role then takes or returns some; the sum stays the same.
-constexpr int MANY_REGS = 128, SOFT_REGS = 160, CONV_REGS = 136, REST_REGS = 56;
+constexpr int MANY_REGS = 96, SOFT_REGS = 152, CONV_REGS = 56, REST_REGS = 56;
+static_assert(SOFT_REGS >= MANY_REGS && CONV_REGS <= MANY_REGS && REST_REGS <= MANY_REGS, "an inc must not lower the count, nor a dec raise it");
 static_assert(SOFT_T * SOFT_REGS + CONV_T * CONV_REGS + 128 * REST_REGS <= MANY_T * MANY_REGS, "registers of the CTA");
 constexpr int OPER = BLK * D * 2;  // bytes of one binary16 operand (hi or lo) of a block
 constexpr uint32_t COL_QH = 0, COL_QL = 64, COL_S = 128, COL_O = 384;
+constexpr int PAGE_RING = 8, PAGE_AHEAD = 3;  // blocks of page numbers held, and written ahead of the scales
 
 struct __align__(1024) ManySmem {
   uint8_t k[2 * OPER];  // hi, lo; [d half][key][64], 128-byte swizzle
   uint8_t v[2 * OPER];
-  float o_sum[64 * SOFT_T];  // kDirect: sum over the folded segments, [dim][thread]
+  uint64_t o_sum[32 * SOFT_T];  // kDirect: sum over the folded segments, [pair of dims][thread]
   // scales of the last 4 blocks: K; V; V 2^E with the whole block's E; running maximum of V in the segment
   float ks[4][BLK], vs[4][BLK], vs2[4][BLK], pm[4][BLK];
-  float2 red[2][2][MANY_ROWS];  // [block parity][half][row]: maximum, and l of the segment that ended
-  uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], o_full, o_empty, sc_full[4], sc_empty[4], pair[4], done;
+  float2 red[2][2][MANY_ROWS];     // [exchange parity][half][row]: maximum, and L of the segment that ended
+  int pages[PAGE_RING][BLK / 16];  // page of every 16 keys (-1: none)
+  uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], o_full, o_empty, sc_full[4], sc_empty[4],
+      row[4], pg_full[PAGE_RING], done;
   uint32_t tmem;
   int abort;
 };
@@ -598,13 +606,125 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Splits two values into binary16 hi and lo pairs (split_plain of each).
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
+// Two fp32 values in one 64-bit register: one instruction for both, each lane
+// rounded as the scalar operation.
+__device__ __forceinline__ uint64_t pk(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpk(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Splits two values into binary16 hi and lo pairs (split_plain of each; the
+// difference as x - 1 hi, rounded once).
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  const float2 v = unpk(x);
+  const __half2 h = __floats2half2_rn(v.x, v.y);
   const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
+  const float2 d = unpk(fma2(pk(f.x, f.y), pk(-1.0f, -1.0f), x));
+  const __half2 l = __floats2half2_rn(d.x, d.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Largest of mx and the 32 scores at TMEM address `src` times the keys' scales
+// (kFull: all of them; else the first nv).
+template <bool kFull>
+__device__ __forceinline__ float score_max(uint32_t src, const float* ks, int nv, float mx) {
+  uint32_t v[32];
+  tmem_ld32(src, v);
+  inv::tmem_wait_ld();
+  const float4* k4 = reinterpret_cast<const float4*>(ks);
+  float m1 = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 k = k4[j];
+    float2 p = unpk(mul2(pk(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), pk(k.x, k.y)));
+    float2 q = unpk(mul2(pk(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), pk(k.z, k.w)));
+    if constexpr (!kFull) {
+      p.x = 4 * j < nv ? p.x : -INFINITY;
+      p.y = 4 * j + 1 < nv ? p.y : -INFINITY;
+      q.x = 4 * j + 2 < nv ? q.x : -INFINITY;
+      q.y = 4 * j + 3 < nv ? q.y : -INFINITY;
+    }
+    mx = max3(mx, p.x, p.y);
+    m1 = max3(m1, q.x, q.y);
+  }
+  return fmaxf(mx, m1);
+}
+
+// Weights of 32 keys: replaces the scores at `src` by w as binary16, 16 columns
+// hi and 16 columns lo, and returns the sum of p (eight interleaved chains, then
+// a tree).  kFull: vs holds the scales times 2^E; else the raw ones, and only
+// the first nv keys have a weight.
+template <bool kFull>
+__device__ __forceinline__ float weights(uint32_t src, const float* ks, const float* vs, int nv, float kap, float mk,
+                                         float vscale) {
+  uint32_t v[32];
+  tmem_ld32(src, v);
+  inv::tmem_wait_ld();
+  const float4* k4 = reinterpret_cast<const float4*>(ks);
+  const float4* v4 = reinterpret_cast<const float4*>(vs);
+  const uint64_t kap2 = pk(kap, kap), mk2 = pk(-mk, -mk);
+  uint64_t s[4];
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 k = k4[j], u = v4[j];
+    const uint64_t kk[2] = {pk(k.x, k.y), pk(k.z, k.w)};
+    uint64_t uu[2] = {pk(u.x, u.y), pk(u.z, u.w)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 4 * j + 2 * i;
+      const uint64_t x = mul2(pk(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), kk[i]);
+      const float2 y = unpk(fma2(x, kap2, mk2));
+      float2 pf = make_float2(inv::ex2(y.x), inv::ex2(y.y));
+      if constexpr (!kFull) {
+        pf.x = e < nv ? pf.x : 0.0f;
+        pf.y = e + 1 < nv ? pf.y : 0.0f;
+        uu[i] = mul2(uu[i], pk(vscale, vscale));
+      }
+      const uint64_t p = pk(pf.x, pf.y);
+      const int c = (2 * j + i) & 3;  // keys 2c, 2c + 1 of every 8
+      s[c] = e < 8 ? p : add2(s[c], p);
+      uint64_t w = mul2(p, uu[i]);
+      if constexpr (!kFull) {  // (a scale behind the row's keys may overflow)
+        const float2 wf = unpk(w);
+        w = pk(e < nv ? wf.x : 0.0f, e + 1 < nv ? wf.y : 0.0f);
+      }
+      split2(w, hi[e >> 1], lo[e >> 1]);
+    }
+  }
+  tmem_st16(src, hi);
+  tmem_st16(src + 16, lo);
+  const float2 a = unpk(s[0]), b = unpk(s[1]), c = unpk(s[2]), d = unpk(s[3]);
+  return __fadd_rn(__fadd_rn(__fadd_rn(a.x, a.y), __fadd_rn(b.x, b.y)),
+                   __fadd_rn(__fadd_rn(c.x, c.y), __fadd_rn(d.x, d.y)));
 }
 
 [[maybe_unused]] __device__ __forceinline__ int64_t cache_rows(const AttnArgs& a) {
@@ -623,11 +743,59 @@ __device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int seq, int h, 
   return (((int64_t)pg * a.c.n_kv_heads + h) << sh) + (key & ((1 << sh) - 1));
 }
 
-// The whole warp waits; false once any wait of the CTA gave up.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, const AttnArgs& a, int* abort) {
-  bool ok = true;
-  if (lane == 0) ok = inv::mbar_wait(bar, parity, a.wait_ns, abort, a.status);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(inv::smem_u32(bar)), "r"(parity), "r"(10000u)
+      : "memory");
+  return ok != 0;
+}
+// A wait that took long: true once it is to be given up.
+__device__ __forceinline__ bool wait_over(unsigned long long& t0, const AttnArgs& a, volatile int* abort) {
+  if (*abort) return true;
+  const unsigned long long now = inv::global_ns();
+  if (t0 == 0) t0 = now;
+  if ((long long)(now - t0) <= a.wait_ns) return false;
+  record_status(a.status, INV_ERR_TIMEOUT);
+  *abort = 1;
+  return true;
+}
+// mbar_wait by a whole warp (kWarp) or one thread, with polls that let the
+// hardware suspend it: the waiting warps share their schedulers with working
+// ones.  False once any wait of the CTA gave up.
+template <bool kWarp>
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, int* abort) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    const bool ok = mbar_poll(bar, parity);
+    if (kWarp ? __all_sync(0xffffffffu, ok) : ok) return true;
+    if ((i & 63u) == 0) {
+      const bool over = wait_over(t0, a, abort);
+      if (kWarp ? __any_sync(0xffffffffu, over) : over) return false;
+    }
+  }
+}
+
+// One arrival for the whole warp, behind all its lanes' accesses.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) inv::mbar_arrive(bar);
+}
+
+// One lane of the warp (a branch on it leaves the MMA operands in uniform
+// registers; on lane == 0 each MMA took 170 clocks to issue instead of 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 template <int kRegs>
@@ -656,23 +824,24 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   ManySmem& sm = *reinterpret_cast<ManySmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    inv::mbar_init(&sm.q_full, SOFT_T);
-    inv::mbar_init(&sm.k_full, CONV_T);
-    inv::mbar_init(&sm.v_full, CONV_T);
+    inv::mbar_init(&sm.q_full, SOFT_T / 32);
+    inv::mbar_init(&sm.k_full, CONV_T / 32);
+    inv::mbar_init(&sm.v_full, CONV_T / 32);
     inv::mbar_init(&sm.k_empty, 1);
     inv::mbar_init(&sm.v_empty, 1);
     inv::mbar_init(&sm.o_full, 1);
-    inv::mbar_init(&sm.o_empty, SOFT_T);
+    inv::mbar_init(&sm.o_empty, SOFT_T / 32);
     inv::mbar_init(&sm.done, 1);
     for (int i = 0; i < 2; ++i) {
       inv::mbar_init(&sm.s_full[i], 1);
-      inv::mbar_init(&sm.p_full[i], SOFT_T);
+      inv::mbar_init(&sm.p_full[i], SOFT_T / 32);
     }
     for (int i = 0; i < 4; ++i) {
-      inv::mbar_init(&sm.sc_full[i], 32);
-      inv::mbar_init(&sm.sc_empty[i], SOFT_T);
-      inv::mbar_init(&sm.pair[i], 64);
+      inv::mbar_init(&sm.sc_full[i], 1);
+      inv::mbar_init(&sm.sc_empty[i], SOFT_T / 32);
+      inv::mbar_init(&sm.row[i], 2);
     }
+    for (int i = 0; i < PAGE_RING; ++i) inv::mbar_init(&sm.pg_full[i], 1);
     sm.abort = 0;
     inv::fence_mbar_init();
   }
@@ -689,7 +858,7 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
   if (warp < SOFT_T / 32) {
     // ================================================================ softmax
     regs_inc<SOFT_REGS>();
-    const int hf = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int hf = warp >> 2, r = (warp & 3) * 32 + lane;  // half of the keys and dims, row
     const int tok = r / G, head = h * G + (r - tok * G);
     const bool valid = tok < t.ntok && tok < per;
     const int nrow = valid ? pos0 + tok + 1 : 0;  // keys the row sees
@@ -706,9 +875,9 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
         m = fmaxf(m, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
       }
       sm.red[0][hf][r].x = m;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(SOFT_T) : "memory");
       m = fmaxf(m, sm.red[0][hf ^ 1][r].x);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(SOFT_T) : "memory");
       const int e = inv::norm_exp(m);
       const float f = inv::pow2f(e);
       kap = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
@@ -718,240 +887,198 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 y = x[8 * c + j];
-          split2(__fmul_rn(y.x, f), __fmul_rn(y.y, f), hi[2 * j], lo[2 * j]);
-          split2(__fmul_rn(y.z, f), __fmul_rn(y.w, f), hi[2 * j + 1], lo[2 * j + 1]);
+          split2(mul2(pk(y.x, y.y), pk(f, f)), hi[2 * j], lo[2 * j]);
+          split2(mul2(pk(y.z, y.w), pk(f, f)), hi[2 * j + 1], lo[2 * j + 1]);
         }
         tmem_st16(lanes + COL_QH + hf * 32 + c * 16, hi);
         tmem_st16(lanes + COL_QL + hf * 32 + c * 16, lo);
       }
       tmem_wait_st();
       inv::tc_fence_before();
-      inv::mbar_arrive(&sm.q_full);
+      warp_arrive(&sm.q_full, lane);
     }
 
-    float O[64];
+    if constexpr (kDirect) {
+#pragma unroll 1
+      for (int j = 0; j < 32; ++j) sm.o_sum[j * SOFT_T + tid] = 0;
+    }
+    uint64_t O[32];  // the segment's sum, dims 64 hf + 2j, + 1
 #pragma unroll
-    for (int j = 0; j < 64; ++j) O[j] = 0.0f;
+    for (int j = 0; j < 32; ++j) O[j] = 0;
     float M = -INFINITY, mk = -INFINITY, L0 = 0.0f, L1 = 0.0f;
     int E = 0;
-    float Mt = -INFINITY, Lt = 0.0f;                 // kDirect: folded segments
-    float beta = 0.0f;                               // of the block whose O is still to be added
-    bool add = false, ends = false;                  // it has keys of this row; it ends a segment
-    float mk_s = 0.0f, l_s = 0.0f;                   // the ended segment's m and l
-    int E_s = 0;
-    uint32_t exch = 0;                               // pair exchanges so far
+    float Mt = -INFINITY, Lt = 0.0f;  // kDirect: folded segments
+    float beta = 0.0f;                // of the block whose O is still to be added
+    bool add = false;                 // that block has keys of the warp's rows
+    uint32_t exch = 0;                // exchanges so far
 
-    // adds block j's O to the sum; at a segment's end passes the segment on
-    const auto fold = [&](int j) {
-      ok = warp_wait(&sm.o_full, j & 1, lane, a, &sm.abort) && ok;
-      inv::tc_fence_after();
-      if (__any_sync(0xffffffffu, add)) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32];
-          tmem_ld32(lanes + COL_O + hf * 64 + c * 32, v);
-          inv::tmem_wait_ld();
-          if (add) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) O[c * 32 + i] = __fmaf_rn(O[c * 32 + i], beta, __uint_as_float(v[i]));
-          }
-        }
-      }
-      inv::tc_fence_before();
-      inv::mbar_arrive(&sm.o_empty);
-      if (!ends) return;
-      const int seg = (b0 + j) / (SEG / BLK);
-      if (ok && nrow > seg * SEG) {
-        const float un = inv::pow2f(1 - E_s);
-        if constexpr (kDirect) {
-          const float Mn = fmaxf(Mt, mk_s);
-          const float fa = seg == 0 ? 0.0f : inv::ex2(__fsub_rn(Mt, Mn)), fb = inv::ex2(__fsub_rn(mk_s, Mn));
-          Mt = Mn;
-          Lt = __fmaf_rn(Lt, fa, __fmul_rn(l_s, fb));
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            float* p = sm.o_sum + i * SOFT_T + tid;
-            *p = __fmaf_rn(seg == 0 ? 0.0f : *p, fa, __fmul_rn(__fmul_rn(O[i], un), fb));
-          }
-        } else {
-          const int64_t rs = part_index(a, t.seq, t.tok0 + tok, t.row0 + tok, head) + seg;
-          if (INV_IN_BOUNDS(a.status, rs, part_count(a))) {
-            float4* po = reinterpret_cast<float4*>(a.part_o + rs * D + hf * 64);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              po[i] = make_float4(__fmul_rn(O[4 * i], un), __fmul_rn(O[4 * i + 1], un), __fmul_rn(O[4 * i + 2], un),
-                                  __fmul_rn(O[4 * i + 3], un));
-            if (hf == 0) a.part_ml[rs] = make_float2(mk_s, l_s);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 64; ++i) O[i] = 0.0f;
-    };
-    // exchanges (maximum, l) with the thread of the row's other half
-    const auto exchange = [&](float2 mine) {
-      sm.red[exch & 1][hf][r] = mine;
-      inv::mbar_arrive(&sm.pair[warp & 3]);
-      ok = warp_wait(&sm.pair[warp & 3], exch & 1, lane, a, &sm.abort) && ok;
-      const float2 other = sm.red[exch & 1][hf ^ 1][r];
-      ++exch;
-      return other;
-    };
-
-    for (int i = 0; i < n && ok; ++i) {
+    // step i: the softmax of block i, then the O of block i - 1, formed meanwhile
+#pragma unroll 1
+    for (int i = 0; i <= n && ok; ++i) {
       const int b = b0 + i, sl = i & 3;
-      const bool first = (b & (SEG / BLK - 1)) == 0;
+      const bool first = (b & (SEG / BLK - 1)) == 0, on = i < n;
+      const bool ends = i > 0 && (first || !on);  // block i - 1 is the last one of its segment
       const uint32_t sc = lanes + COL_S + (i & 1) * 128 + hf * 64;
-      const int nv = min(BLK, nrow - b * BLK) - hf * 64;  // visible keys among this thread's 64 (may be <= 0 or > 64)
-      const bool row_on = nrow > b * BLK;
-      const bool any = __any_sync(0xffffffffu, row_on), full = __all_sync(0xffffffffu, nrow >= (b + 1) * BLK);
-      ok = warp_wait(&sm.sc_full[sl], (i >> 2) & 1, lane, a, &sm.abort) && ok;
-      ok = warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, lane, a, &sm.abort) && ok;
-      inv::tc_fence_after();
+      const int nv = nrow - b * BLK - hf * 64;  // visible keys among this thread's 64 (may be <= 0 or > 64)
+      const bool row_on = on && nrow > b * BLK;
+      const bool any = __any_sync(0xffffffffu, row_on);
+      const bool full = on && __all_sync(0xffffffffu, nrow >= (b + 1) * BLK);
+      const float* ks = sm.ks[sl] + hf * 64;
       float mx = -INFINITY;
-      if (any) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32];
-          tmem_ld32(sc + c * 32, v);
-          inv::tmem_wait_ld();
-          const float* ks = sm.ks[sl] + hf * 64 + c * 32;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x = __fmul_rn(__uint_as_float(v[j]), ks[j]);
-            mx = fmaxf(mx, full || c * 32 + j < nv ? x : -INFINITY);
-          }
+      if (on) {
+        ok = bar_wait<true>(&sm.sc_full[sl], (i >> 2) & 1, a, &sm.abort) && ok;
+        ok = bar_wait<true>(&sm.s_full[i & 1], (i >> 1) & 1, a, &sm.abort) && ok;
+        inv::tc_fence_after();
+        if (full) {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) mx = score_max<true>(sc + c, ks + c, 32, mx);
+        } else if (any) {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) mx = score_max<false>(sc + c, ks + c, nv - c, mx);
         }
       }
-      const bool starts = first && i > 0;
-      const float mk_old = mk;
-      const int E_old = E;
-      const bool add_old = add, ends_old = starts;
-      const float beta_old = beta;
-      if (any || starts) {
+      // the row's other half: its maximum, and the L of the segment that ended
+      const float mk_s = mk;
+      const int E_s = E;
+      float l_s = 0.0f;
+      if (any || ends) {
         const float lh = __fadd_rn(L0, L1);
-        const float2 other = exchange(make_float2(mx, lh));
+        sm.red[exch & 1][hf][r] = make_float2(mx, lh);
+        warp_arrive(&sm.row[warp & 3], lane);
+        ok = bar_wait<true>(&sm.row[warp & 3], exch & 1, a, &sm.abort) && ok;
+        const float2 other = sm.red[exch & 1][hf ^ 1][r];
+        ++exch;
         mx = fmaxf(mx, other.x);
-        if (starts) {
-          mk_s = mk;
-          E_s = E;
-          l_s = hf == 0 ? __fadd_rn(lh, other.y) : __fadd_rn(other.y, lh);
+        l_s = __fadd_rn(lh, other.y);  // (L_0 + L_1) + (L_2 + L_3) on either side
+      }
+      float beta_n = 1.0f;
+      if (on) {
+        if (first) {
+          M = -INFINITY;
+          L0 = L1 = 0.0f;
         }
-      }
-      if (first) {
-        M = -INFINITY;
-        L0 = L1 = 0.0f;
-      }
-      add = row_on;
-      beta = 1.0f;
-      if (row_on) {
-        M = fmaxf(M, mx);
-        mk = __fmul_rn(M, kap);
-        E = inv::norm_exp(sm.pm[sl][min(BLK, nrow - b * BLK) - 1]);
-        const float alpha = first ? 0.0f : inv::ex2(__fsub_rn(mk_old, mk));
-        beta = first ? 0.0f : __fmul_rn(alpha, inv::pow2f(max(E - E_old, -126)));
-        L0 = __fmul_rn(L0, alpha);
-        L1 = __fmul_rn(L1, alpha);
-      }
-      if (any) {
-        const float vscale = inv::pow2f(E);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32];
-          tmem_ld32(sc + c * 32, v);
-          inv::tmem_wait_ld();
-          const float* ks = sm.ks[sl] + hf * 64 + c * 32;
-          const float* vs = (full ? sm.vs2[sl] : sm.vs[sl]) + hf * 64 + c * 32;
-          float s[8];
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float p[2], w[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              p[u] = 0.0f;
-              w[u] = 0.0f;
-              if (full || c * 32 + j + u < nv) {
-                p[u] = inv::ex2(__fmaf_rn(__fmul_rn(__uint_as_float(v[j + u]), ks[j + u]), kap, -mk));
-                w[u] = __fmul_rn(p[u], full ? vs[j + u] : __fmul_rn(vs[j + u], vscale));
-              }
-              s[(j + u) & 7] = j + u < 8 ? p[u] : __fadd_rn(s[(j + u) & 7], p[u]);
-            }
-            split2(w[0], w[1], hi[j >> 1], lo[j >> 1]);
+        if (row_on) {
+          M = fmaxf(M, mx);
+          mk = __fmul_rn(M, kap);
+          E = inv::norm_exp(sm.pm[sl][min(BLK, nrow - b * BLK) - 1]);
+          const float alpha = first ? 0.0f : inv::ex2(__fsub_rn(mk_s, mk));
+          beta_n = first ? 0.0f : __fmul_rn(alpha, inv::pow2f(max(E - E_s, -126)));
+          L0 = __fmul_rn(L0, alpha);
+          L1 = __fmul_rn(L1, alpha);
+        }
+        float g = 0.0f;
+        if (full) {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            if (c != 0) L0 = __fadd_rn(L0, g);
+            g = weights<true>(sc + c, ks + c, sm.vs2[sl] + hf * 64 + c, 32, kap, mk, 1.0f);
           }
-          const float g = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])),
-                                    __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
-          if (c == 0)
-            L0 = __fadd_rn(L0, g);
-          else
-            L1 = __fadd_rn(L1, g);
-          tmem_st16(sc + c * 32, hi);
-          tmem_st16(sc + c * 32 + 16, lo);
+        } else if (any) {
+          const float vscale = inv::pow2f(E);
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            if (c != 0) L0 = __fadd_rn(L0, g);
+            g = weights<false>(sc + c, ks + c, sm.vs[sl] + hf * 64 + c, nv - c, kap, mk, vscale);
+          }
         }
+        L1 = __fadd_rn(L1, g);
         tmem_wait_st();
+        inv::tc_fence_before();
+        warp_arrive(&sm.p_full[i & 1], lane);
+        if (lane == 0) inv::mbar_arrive(&sm.sc_empty[sl]);
       }
-      inv::tc_fence_before();
-      inv::mbar_arrive(&sm.p_full[i & 1]);
-      inv::mbar_arrive(&sm.sc_empty[sl]);
-      if (i > 0) {  // the previous block's O, formed during this softmax
-        const float beta_new = beta;
-        const bool add_new = add;
-        beta = beta_old;
-        add = add_old;
-        ends = ends_old;
-        fold(i - 1);
-        beta = beta_new;
-        add = add_new;
-      }
-    }
-    if (ok) {
-      const float lh = __fadd_rn(L0, L1);
-      const float2 other = exchange(make_float2(0.0f, lh));
-      mk_s = mk;
-      E_s = E;
-      l_s = hf == 0 ? __fadd_rn(lh, other.y) : __fadd_rn(other.y, lh);
-      ends = true;
-      fold(n - 1);
-      if constexpr (kDirect) {
-        if (ok && nrow > 0) {
-          const float il = __frcp_rn(Lt);
-          const int64_t io = ((int64_t)(t.row0 + tok) * a.Hq + head) * D + hf * 64;
-          if (INV_SPAN_IN_BOUNDS(a.status, io, io + 63, (int64_t)a.T * a.Hq * D)) {
+      if (i > 0) {
+        ok = bar_wait<true>(&sm.o_full, (i - 1) & 1, a, &sm.abort) && ok;
+        inv::tc_fence_after();
+        if (add) {  // (a row without keys in the block has weights 0 and beta 1)
+          const uint64_t b2 = pk(beta, beta);
 #pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-              const float* p = sm.o_sum + i * SOFT_T + tid;
-              store_out4(a, io + i, make_float4(__fmul_rn(p[0], il), __fmul_rn(p[SOFT_T], il),
-                                                __fmul_rn(p[2 * SOFT_T], il), __fmul_rn(p[3 * SOFT_T], il)));
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32];
+            tmem_ld32(lanes + COL_O + hf * 64 + c * 32, v);
+            inv::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              O[16 * c + j] = fma2(O[16 * c + j], b2, pk(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])));
+          }
+        }
+        inv::tc_fence_before();
+        warp_arrive(&sm.o_empty, lane);
+        if (ends) {  // passes the segment on
+          const int seg = (b - 1) / (SEG / BLK);
+          if (ok && nrow > seg * SEG) {
+            const float un = inv::pow2f(1 - E_s);
+            const uint64_t un2 = pk(un, un);
+            if constexpr (kDirect) {
+              const float Mn = fmaxf(Mt, mk_s);
+              const float fa = seg == 0 ? 0.0f : inv::ex2(__fsub_rn(Mt, Mn)), fb = inv::ex2(__fsub_rn(mk_s, Mn));
+              Mt = Mn;
+              Lt = __fmaf_rn(Lt, fa, __fmul_rn(l_s, fb));
+              const uint64_t fa2 = pk(fa, fa), fb2 = pk(fb, fb);
+              uint64_t* p = sm.o_sum + tid;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                p[j * SOFT_T] = fma2(p[j * SOFT_T], fa2, mul2(mul2(O[j], un2), fb2));
+            } else {
+              const int64_t rs = part_index(a, t.seq, t.tok0 + tok, t.row0 + tok, head) + seg;
+              if (INV_IN_BOUNDS(a.status, rs, part_count(a))) {
+                float4* po = reinterpret_cast<float4*>(a.part_o + rs * D + hf * 64);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float2 x = unpk(mul2(O[2 * j], un2)), y = unpk(mul2(O[2 * j + 1], un2));
+                  po[j] = make_float4(x.x, x.y, y.x, y.y);
+                }
+                if (hf == 0) a.part_ml[rs] = make_float2(mk_s, l_s);
+              }
             }
+          }
+        }  // (the next segment's first block has beta 0)
+      }
+      beta = beta_n;
+      add = any;
+    }
+    if constexpr (kDirect) {
+      if (ok && nrow > 0) {
+        const float il = __frcp_rn(Lt);
+        const int64_t io = ((int64_t)(t.row0 + tok) * a.Hq + head) * D + hf * 64;
+        if (INV_SPAN_IN_BOUNDS(a.status, io, io + 63, (int64_t)a.T * a.Hq * D)) {
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t* p = sm.o_sum + 2 * j * SOFT_T + tid;
+            const float2 x = unpk(mul2(p[0], pk(il, il))), y = unpk(mul2(p[SOFT_T], pk(il, il)));
+            store_out4(a, io + 4 * j, make_float4(x.x, x.y, y.x, y.y));
           }
         }
       }
     }
   } else if (warp < MMA_WARP) {
     // ============================================================= converters
-    regs_inc<CONV_REGS>();
-    const int ct = tid - SOFT_T, kr = ct >> 4, ch = ct & 15;  // key kr of every 8, dims 8 ch .. 8 ch + 7
-    // half an operand (64 keys from kh on) of block i into registers
-    const auto load = [&](const int16_t* codes, int i, int kh, uint4 (&x)[8]) {
+    regs_dec<CONV_REGS>();
+    const int ct = tid - SOFT_T, kr = ct >> 4, ch = ct & 15;  // key kr of every 16, dims 8 ch .. 8 ch + 7
+    const int Hkv = a.c.n_kv_heads, sh = a.c.page_shift, ps = 1 << sh;
+    // half an operand (64 keys from kh on) of block i into registers; 16 keys lie in one page
+    const auto load = [&](const int16_t* codes, int i, int kh, uint4 (&x)[4]) {
+      const int key0 = (b0 + i) * BLK + kh + kr;
+      const int* pages = sm.pages[i % PAGE_RING] + kh / 16;
+      const uint4* src = reinterpret_cast<const uint4*>(codes) + ch;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t row = cache_row(a, t.seq, h, (b0 + i) * BLK + kh + 8 * j + kr, last);
-        const bool in = row >= 0 && INV_IN_BOUNDS(a.status, row, cache_rows(a));
-        x[j] = in ? __ldg(reinterpret_cast<const uint4*>(codes + row * D) + ch) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        const int key = key0 + 16 * j, pg = pages[j];
+        const int row = ((pg * Hkv + h) << sh) + (key & (ps - 1));  // below 2^31 for a page of the cache
+        const bool in = pg >= 0 && key < last && INV_IN_BOUNDS(a.status, row, cache_rows(a));
+        x[j] = in ? __ldg(src + (int64_t)row * 16) : make_uint4(0, 0, 0, 0);
       }
     };
-    const auto store = [&](uint8_t* dst, int kh, const uint4 (&x)[8]) {
+    const uint32_t dst0 = (ch >> 3) * (BLK * 128) + kr * 128 + (((ch & 7) ^ (kr & 7)) << 4);
+    const auto store = [&](uint8_t* dst, const uint4 (&x)[4]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = kh + 8 * j + kr;
+      for (int j = 0; j < 4; ++j) {
         uint4 hi, lo;
         inv::unpack_code(x[j].x, hi.x, lo.x);
         inv::unpack_code(x[j].y, hi.y, lo.y);
         inv::unpack_code(x[j].z, hi.z, lo.z);
         inv::unpack_code(x[j].w, hi.w, lo.w);
-        uint8_t* p = dst + (ch >> 3) * (BLK * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
-        *reinterpret_cast<uint4*>(p) = hi;
-        *reinterpret_cast<uint4*>(p + OPER) = lo;
+        *reinterpret_cast<uint4*>(dst + j * 2048) = hi;  // 16 keys on
+        *reinterpret_cast<uint4*>(dst + j * 2048 + OPER) = lo;
       }
     };
     // Operands in the order they can be stored: K 0, then K i+1 (free once S(i) is formed) before V i (free once
@@ -960,27 +1087,51 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
       is_v = s > 0 && (!(s & 1) || s == 2 * n - 1);
       return s == 0 ? 0 : (s & 1) ? (s == 2 * n - 1 ? n - 1 : (s + 1) / 2) : s / 2 - 1;
     };
-    uint4 xa[8], xb[8];
-    load(a.c.k, 0, 0, xa);
-    load(a.c.k, 0, 64, xb);
-    for (int s = 0; s < 2 * n && ok; ++s) {
-      bool is_v, next_v = false;
-      const int i = operand(s, is_v), ni = s + 1 < 2 * n ? operand(s + 1, next_v) : 0;
-      const int16_t* next = next_v ? a.c.v : a.c.k;
-      if (i > 0) ok = warp_wait(is_v ? &sm.v_empty : &sm.k_empty, (i - 1) & 1, lane, a, &sm.abort) && ok;
-      uint8_t* dst = is_v ? sm.v : sm.k;
-      store(dst, 0, xa);
-      if (s + 1 < 2 * n) load(next, ni, 0, xa);
-      store(dst, 64, xb);
-      if (s + 1 < 2 * n) load(next, ni, 64, xb);
-      inv::fence_proxy_async_smem();
-      inv::mbar_arrive(is_v ? &sm.v_full : &sm.k_full);
+    // half s & 1 of operand s >> 1, with the next half's codes on their way
+    uint4 x[4], y[4];
+    ok = bar_wait<true>(&sm.pg_full[0], 0, a, &sm.abort) && ok;
+    load(a.c.k, 0, 0, x);
+    load(a.c.k, 0, 64, y);
+#pragma unroll 1
+    for (int s = 0; s < 4 * n && ok; ++s) {
+      bool is_v, next_v;
+      const int i = operand(s >> 1, is_v);
+      if ((s & 1) == 0 && i > 0) ok = bar_wait<true>(is_v ? &sm.v_empty : &sm.k_empty, (i - 1) & 1, a, &sm.abort) && ok;
+      store((is_v ? sm.v : sm.k) + dst0 + (s & 1) * (64 * 128), x);
+      if (s & 1) {
+        inv::fence_proxy_async_smem();
+        warp_arrive(is_v ? &sm.v_full : &sm.k_full, lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = y[j];
+      if (s + 2 < 4 * n) {
+        const int ni = operand((s + 2) >> 1, next_v);
+        if (!next_v && (s & 1) == 0)
+          ok = bar_wait<true>(&sm.pg_full[ni % PAGE_RING], (ni / PAGE_RING) & 1, a, &sm.abort) && ok;
+        load(next_v ? a.c.v : a.c.k, ni, (s & 1) * 64, y);
+      }
     }
   } else {
     regs_dec<REST_REGS>();
     if (warp == SCALE_WARP) {
     // ================================================================= scales
     float carry = 0.0f;  // largest V scale of the segment so far
+    // Page numbers of block j.  Its slot held block j - 8's, whose V was loaded before K of block j - 7 was stored:
+    // before the softmax of block j - 7 <= i - 4.
+    const auto put_pages = [&](int j) {
+      if (lane < BLK / 16) {
+        const int key = (b0 + j) * BLK + 16 * lane;
+        int pg = key < last ? a.rb.page_table[t.seq * a.rb.ld_table + (key >> a.c.page_shift)] : -1;
+        if (key < last && (pg < 0 || pg >= a.c.n_pages)) {
+          record_status(a.status, INV_ERR_INVALID_ARG);
+          pg = -1;
+        }
+        sm.pages[j % PAGE_RING][lane] = pg;
+      }
+      warp_arrive(&sm.pg_full[j % PAGE_RING], lane);
+    };
+    for (int j = 0; j < min(n, PAGE_AHEAD); ++j) put_pages(j);
+#pragma unroll 1
     for (int i = 0; i < n && ok; ++i) {
       // keys 4 lane .. 4 lane + 3 of the block (one page)
       float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
@@ -1000,7 +1151,7 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
       pv.z = fmaxf(pv.y, vv.z);
       pv.w = fmaxf(pv.z, vv.w);
       float up = pv.w;
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const float x = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up = fmaxf(up, x);
@@ -1009,66 +1160,67 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
       before = fmaxf(lane == 0 ? 0.0f : before, carry);
       carry = fmaxf(carry, __shfl_sync(0xffffffffu, up, 31));
       const float f = inv::pow2f(inv::norm_exp(carry));
-      if (i >= 4) ok = warp_wait(&sm.sc_empty[sl], ((i - 4) >> 2) & 1, lane, a, &sm.abort) && ok;
+      if (i >= 4) ok = bar_wait<true>(&sm.sc_empty[sl], ((i - 4) >> 2) & 1, a, &sm.abort) && ok;
+      if (i + PAGE_AHEAD < n) put_pages(i + PAGE_AHEAD);
       reinterpret_cast<float4*>(sm.ks[sl])[lane] = kv;
       reinterpret_cast<float4*>(sm.vs[sl])[lane] = vv;
       reinterpret_cast<float4*>(sm.vs2[sl])[lane] =
           make_float4(__fmul_rn(vv.x, f), __fmul_rn(vv.y, f), __fmul_rn(vv.z, f), __fmul_rn(vv.w, f));
       reinterpret_cast<float4*>(sm.pm[sl])[lane] =
           make_float4(fmaxf(pv.x, before), fmaxf(pv.y, before), fmaxf(pv.z, before), fmaxf(pv.w, before));
-      inv::mbar_arrive(&sm.sc_full[sl]);
+      warp_arrive(&sm.sc_full[sl], lane);
     }
-    } else if (warp == MMA_WARP && lane == 0) {
+    } else if (warp == MMA_WARP && elect_one()) {
     // ==================================================================== MMA
     constexpr uint32_t ID_S = inv::idesc_f16_f32(MANY_ROWS, BLK);
     constexpr uint32_t ID_O = inv::idesc_f16_f32(MANY_ROWS, D) | (1u << 16);  // B is MN-major
-    const uint32_t kb = inv::smem_u32(sm.k), vb = inv::smem_u32(sm.v);
+    const uint64_t kdesc = inv::sw128_kmajor_desc(inv::smem_u32(sm.k));
+    const uint64_t vdesc = sw128_mnmajor_desc(inv::smem_u32(sm.v), BLK * 128, 1024);
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && inv::mbar_wait(bar, parity, a.wait_ns, &sm.abort, a.status);
-    };
-    const auto scores = [&](int i) {
-      wait(&sm.k_full, i & 1);
-      if (!ok) return;
-      inv::tc_fence_after();
-      const uint32_t d = tm + COL_S + (i & 1) * 128;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t off = (k >> 2) * (BLK * 128) + (k & 3) * 32;
-        umma_ts(d, tm + COL_QH + 8 * k, inv::sw128_kmajor_desc(kb + OPER + off), ID_S, k != 0);
-        umma_ts(d, tm + COL_QL + 8 * k, inv::sw128_kmajor_desc(kb + off), ID_S, 1);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_ts(d, tm + COL_QH + 8 * k, inv::sw128_kmajor_desc(kb + (k >> 2) * (BLK * 128) + (k & 3) * 32), ID_S, 1);
-      inv::umma_commit(&sm.k_empty);
-      inv::umma_commit(&sm.s_full[i & 1]);
-    };
-    const auto values = [&](int i) {
-      wait(&sm.p_full[i & 1], (i >> 1) & 1);
-      wait(&sm.v_full, i & 1);
-      if (i > 0) wait(&sm.o_empty, (i - 1) & 1);
-      if (!ok) return;
-      inv::tc_fence_after();
-      const uint32_t w0 = tm + COL_S + (i & 1) * 128, d = tm + COL_O;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w = w0 + (k >> 1) * 32 + (k & 1) * 8;  // hi; lo 16 columns on
-        umma_ts(d, w, sw128_mnmajor_desc(vb + OPER + k * 2048, BLK * 128, 1024), ID_O, k != 0);
-        umma_ts(d, w + 16, sw128_mnmajor_desc(vb + k * 2048, BLK * 128, 1024), ID_O, 1);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_ts(d, w0 + (k >> 1) * 32 + (k & 1) * 8, sw128_mnmajor_desc(vb + k * 2048, BLK * 128, 1024), ID_O, 1);
-      inv::umma_commit(&sm.v_empty);
-      inv::umma_commit(&sm.o_full);
+      ok = ok && bar_wait<false>(bar, parity, a, &sm.abort);
     };
     wait(&sm.q_full, 0);
-    scores(0);
-    for (int i = 1; i < n && ok; ++i) {
-      scores(i);
-      values(i - 1);
+#pragma unroll 1
+    for (int i = 0; i <= n && ok; ++i) {
+      if (i < n) {  // scores of block i
+        wait(&sm.k_full, i & 1);
+        if (!ok) break;
+        inv::tc_fence_after();
+        const uint32_t d = tm + COL_S + (i & 1) * 128;
+        // operands advance by 32 bytes a step of 16 dims, and to the second half of d after 4
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t b = kdesc + (k >> 2) * (BLK * 128 >> 4) + (k & 3) * 2;
+          umma_ts(d, tm + COL_QH + 8 * k, b + (OPER >> 4), ID_S, k != 0);
+          umma_ts(d, tm + COL_QL + 8 * k, b, ID_S, 1);
+        }
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k)
+          umma_ts(d, tm + COL_QH + 8 * k, kdesc + (k >> 2) * (BLK * 128 >> 4) + (k & 3) * 2, ID_S, 1);
+        inv::umma_commit(&sm.k_empty);
+        inv::umma_commit(&sm.s_full[i & 1]);
+      }
+      if (i > 0) {  // O of block i - 1
+        const int j = i - 1;
+        wait(&sm.p_full[j & 1], (j >> 1) & 1);
+        wait(&sm.v_full, j & 1);
+        if (j > 0) wait(&sm.o_empty, (j - 1) & 1);
+        if (!ok) break;
+        inv::tc_fence_after();
+        const uint32_t w0 = tm + COL_S + (j & 1) * 128, d = tm + COL_O;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t w = w0 + (k >> 1) * 32 + (k & 1) * 8;  // hi; lo 16 columns on
+          const uint64_t b = vdesc + k * (2048 >> 4);
+          umma_ts(d, w, b + (OPER >> 4), ID_O, k != 0);
+          umma_ts(d, w + 16, b, ID_O, 1);
+        }
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) umma_ts(d, w0 + (k >> 1) * 32 + (k & 1) * 8, vdesc + k * (2048 >> 4), ID_O, 1);
+        inv::umma_commit(&sm.v_empty);
+        inv::umma_commit(&sm.o_full);
+      }
     }
-    if (ok) values(n - 1);
     // every MMA has finished before tensor memory is given back
     inv::umma_commit(&sm.done);
     inv::mbar_wait(&sm.done, 0, a.wait_ns, nullptr, a.status);
