@@ -11,12 +11,14 @@
 //   x_j    = acc_j s_K,j;   kappa = (sigma log2 e) 2^(1-e)
 //   per block of 128 keys: M' = max(M, max_j x_j), mk = M' kappa,
 //            p_j = 2^(x_j kappa - mk), alpha = 2^(mk_old - mk);
-//            L_g <- L_g alpha + (sum of p over the 32-key group g)
+//            L_g <- L_g alpha + (sum of p over the 16-key group g: key k and
+//            k + 8 first, then a tree over k: k xor 2, xor 4, xor 1)
 //            w_j = p_j (s_V,j 2^E), 2^E from the largest s_V of the segment's
 //            keys seen so far (brought into [2^13, 2^14)), w = w_hi + w_lo;
 //            O  <- O alpha 2^(E - E_old) + sum_j w_j code_j / 2, the sum again
 //            cross products first, over keys in steps of 16;
-//   segment of 512 keys: o = O 2^(1-E), l = (L_0 + L_1) + (L_2 + L_3), m = mk;
+//   segment of 512 keys: o = O 2^(1-E), l = ((L_0 + L_1) + (L_2 + L_3)) +
+//            ((L_4 + L_5) + (L_6 + L_7)), m = mk;
 //   segments folded in ascending order with the same running maximum.
 // A tensor-core product sum depends neither on the other rows or columns of
 // its tile nor on whether mma.sync or tcgen05.mma forms it (checked bit for
@@ -139,24 +141,28 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, in
 
 // ------------------------------------------------------- few rows: mma.sync --
 //
-// One CTA (4 warps) per (sequence of at most 8 NT rows, kv head, segment).  A
-// row is a (token, query head of the group) pair.  K and V blocks of 128 keys stream
-// through a ring of 32 KB slots (2-D TMA, 128-byte swizzle, one box per page
-// and half of d).  S^T = K Q^T: warp w owns keys 32w .. 32w+31 of the block
-// (rows of two m-tiles), the tile's rows are the MMA columns.  O^T = V^T W:
-// warp w owns dims 32w .. 32w+31.  W crosses the warps through shared memory.
-constexpr int TH = 128;
-constexpr int SLOT = BLK * D * 2;      // 32 KB: codes of one block
-constexpr int PSTR = BLK + 8;          // halfs per row of the w and q arrays (conflict-free fragments)
+// One CTA (8 warps) per (sequence of at most 8 NT rows, kv head, segment).  A
+// row is a (token, query head of the group) pair.  K and V blocks of 128 keys
+// stream through a ring of NST 32 KB slots (2-D TMA, 128-byte swizzle, one box
+// per page and half of d).  S^T = K Q^T: warp w owns keys 16w .. 16w+15 of the
+// block (the rows of an m-tile), the tile's rows are the MMA columns.  O^T = V^T
+// W: warp w owns dims 16w .. 16w+15.  W crosses the warps through shared memory.
+constexpr int TH = 256, FEW_WARPS = TH / 32;
+constexpr int SLOT = BLK * D * 2;  // 32 KB: codes of one block
+
+// B fragments of 8 rows: lane (g, c) of k-step k holds, for row g, the pairs
+// (16k + 2c, + 1) and (16k + 2c + 8, + 9), hi and lo: {hi0, hi1, lo0, lo1}.
+struct Frags {
+  uint4 f[8][32];
+};
 
 template <int NT, int NST>
 struct __align__(1024) FewSmem {
   uint8_t ring[NST * SLOT];
-  __half qh[8 * NT * PSTR], ql[8 * NT * PSTR];
-  __half wh[8 * NT * PSTR], wl[8 * NT * PSTR];
+  Frags q[NT], w[NT];
   float ks[SEG], vs[SEG], pm[SEG];
-  float red_m[4][8 * NT];
-  float red_l[4][8 * NT];
+  float red_m[FEW_WARPS][8 * NT];
+  float red_l[FEW_WARPS][8 * NT];
   float kappa[8 * NT];
   int pages[SEG / 16];
   uint64_t full[NST];
@@ -170,19 +176,18 @@ __device__ __forceinline__ uint32_t code_addr(uint32_t base, int r, int d0) {
 }
 
 template <int NT, int NST>
-__global__ void __launch_bounds__(TH)
+__global__ void __launch_bounds__(TH, 2)
     attn_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ AttnArgs a) {
   inv::grid_launch_dependents();  // the fold may be scheduled once every CTA has started
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int seg = blockIdx.x % a.S_max, h = blockIdx.y;
-  const int G = a.G, per = (8 * NT) / G, Hkv = a.c.n_kv_heads;
+  const int G = a.G, Hkv = a.c.n_kv_heads;
   Tile t;
-  if (!load_seq(a, blockIdx.x / a.S_max, lane, t) || t.n_new > min(a.few, per)) return;
-  t.tok0 = 0;
-  t.ntok = t.n_new;
-  const int pos0 = t.len - t.n_new + t.tok0;           // position of the tile's first token
-  const int key0 = seg * SEG, last = pos0 + t.ntok;    // keys of the tile: 0 .. last - 1
+  if (!load_seq(a, blockIdx.x / a.S_max, lane, t) || t.n_new > a.few || t.n_new * G > 8 * NT) return;
+  const int rows = t.n_new * G;
+  const int pos0 = t.len - t.n_new;                // position of the first new token
+  const int key0 = seg * SEG, last = t.len;        // the rows see keys 0 .. last - 1 at most
   if (key0 >= last) return;
   const int n_keys = min(SEG, last - key0), nblk = (n_keys + BLK - 1) / BLK;
 
@@ -218,6 +223,7 @@ __global__ void __launch_bounds__(TH)
     const int kn = min(BLK, n_keys - b * BLK), box = min(ps, BLK), nb = (kn + box - 1) / box;
     inv::mbar_arrive_expect_tx(&sm.full[s], nb * box * D * 2);
     const CUtensorMap* tm = (i & 1) ? &tm_v : &tm_k;
+#pragma unroll 1
     for (int j = 0; j < nb; ++j) {
       const int kk = key0 + b * BLK + j * box;  // first key of the box
       const int row = (sm.pages[(kk - key0) >> sh] * Hkv + h) * ps + (kk & (ps - 1));
@@ -227,31 +233,26 @@ __global__ void __launch_bounds__(TH)
     }
   };
   int issued = 0;
-  if (tid == 0)
+  if (tid == 0) {
+#pragma unroll 1
     for (; issued < NST && issued < items; ++issued) issue(issued);
+  }
 
   // scales of the segment (zero behind its last key), and their running maximum
   {
-    float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-    const int j = 4 * tid;  // keys j .. j+3: one page (page sizes are multiples of 16)
+    float2 kv = make_float2(0.f, 0.f), vv = kv;
+    const int j = 2 * tid;  // keys j, j + 1: one page
     if (j < n_keys) {
       const int64_t row = ((int64_t)sm.pages[j >> sh] * Hkv + h) * ps + ((key0 + j) & (ps - 1));
-      if (INV_SPAN_IN_BOUNDS(a.status, row, row + 3, (int64_t)a.c.n_pages * Hkv * ps)) {
-        kv = *reinterpret_cast<const float4*>(a.c.k_scale + row);
-        vv = *reinterpret_cast<const float4*>(a.c.v_scale + row);
+      if (INV_SPAN_IN_BOUNDS(a.status, row, row + 1, (int64_t)a.c.n_pages * Hkv * ps)) {
+        kv = *reinterpret_cast<const float2*>(a.c.k_scale + row);
+        vv = *reinterpret_cast<const float2*>(a.c.v_scale + row);
       }
       if (j + 1 >= n_keys) kv.y = vv.y = 0.0f;
-      if (j + 2 >= n_keys) kv.z = vv.z = 0.0f;
-      if (j + 3 >= n_keys) kv.w = vv.w = 0.0f;
     }
-    *reinterpret_cast<float4*>(sm.ks + j) = kv;
-    *reinterpret_cast<float4*>(sm.vs + j) = vv;
-    float4 pv;
-    pv.x = vv.x;
-    pv.y = fmaxf(pv.x, vv.y);
-    pv.z = fmaxf(pv.y, vv.z);
-    pv.w = fmaxf(pv.z, vv.w);
-    float up = pv.w;
+    *reinterpret_cast<float2*>(sm.ks + j) = kv;
+    *reinterpret_cast<float2*>(sm.vs + j) = vv;
+    float up = fmaxf(vv.x, vv.y);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const float x = __shfl_up_sync(0xffffffffu, up, o);
@@ -262,17 +263,15 @@ __global__ void __launch_bounds__(TH)
     if (lane == 0) before = 0.0f;
     __syncthreads();
     for (int w = 0; w < warp; ++w) before = fmaxf(before, sm.red_m[0][w]);
-    pv.x = fmaxf(pv.x, before);
-    pv.y = fmaxf(pv.y, before);
-    pv.z = fmaxf(pv.z, before);
-    pv.w = fmaxf(pv.w, before);
-    *reinterpret_cast<float4*>(sm.pm + j) = pv;
+    const float p0 = fmaxf(before, vv.x);
+    *reinterpret_cast<float2*>(sm.pm + j) = make_float2(p0, fmaxf(p0, vv.y));
   }
-  // the tile's q rows: scaled by 2^e, split
-  for (int r = warp; r < 8 * NT; r += 4) {
+  // the rows' q, scaled by 2^e and split; lane holds dims 4 lane .. 4 lane + 3
+#pragma unroll 1
+  for (int r = warp; r < 8 * NT; r += FEW_WARPS) {
     const int tok = r / G, head = r - tok * G;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tok < t.ntok && tok < per) {
+    if (r < rows) {
       const int64_t iq = (int64_t)(t.row0 + tok) * a.ld_q + (int64_t)(h * G + head) * D;
       if (INV_SPAN_IN_BOUNDS(a.status, iq, iq + D - 1, (int64_t)(a.T - 1) * a.ld_q + (int64_t)a.Hq * D))
         x = reinterpret_cast<const float4*>(a.q + iq)[lane];
@@ -287,29 +286,32 @@ __global__ void __launch_bounds__(TH)
     inv::split_plain(__fmul_rn(x.y, f), hi[1], lo[1]);
     inv::split_plain(__fmul_rn(x.z, f), hi[2], lo[2]);
     inv::split_plain(__fmul_rn(x.w, f), hi[3], lo[3]);
-    *reinterpret_cast<uint2*>(sm.qh + r * PSTR + 4 * lane) = make_uint2(pack_half2(hi[0], hi[1]), pack_half2(hi[2], hi[3]));
-    *reinterpret_cast<uint2*>(sm.ql + r * PSTR + 4 * lane) = make_uint2(pack_half2(lo[0], lo[1]), pack_half2(lo[2], lo[3]));
+    // dims 4 lane, + 1 and + 2, + 3: k-step lane / 4, pair of c = 2 (lane % 2), + 1 of its half (lane % 4) / 2
+    uint32_t* dst = reinterpret_cast<uint32_t*>(&sm.q[r >> 3].f[lane >> 2][4 * (r & 7) + 2 * (lane & 1)]) + ((lane >> 1) & 1);
+    dst[0] = pack_half2(hi[0], hi[1]);
+    dst[2] = pack_half2(lo[0], lo[1]);
+    dst[4] = pack_half2(hi[2], hi[3]);
+    dst[6] = pack_half2(lo[2], lo[3]);
     if (lane == 0) sm.kappa[r] = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
   }
   __syncthreads();
 
-  // state of the rows 2c, 2c + 1 of every n-tile (the same in all lanes and warps that share c)
+  // state of the rows 2c, 2c + 1 of every n-tile (the same in all lanes and warps that share c; L is the warp's)
   float kap[NT][2], M[NT][2], mk[NT][2], L[NT][2];
   int E[NT][2], nrow[NT][2];  // nrow: keys of the row in the segment
-  float o[NT][2][4];          // O of dims 32 warp + 16 mt + g (+8), rows 2c, 2c + 1
+  float o[NT][4];             // O of dims 16 warp + g (+8), rows 2c, 2c + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = 8 * nt + 2 * c + i, tok = r / G;
+      const int r = 8 * nt + 2 * c + i;
       kap[nt][i] = sm.kappa[r];
-      nrow[nt][i] = tok < t.ntok && tok < per ? min(SEG, pos0 + tok + 1 - key0) : 0;
+      nrow[nt][i] = r < rows ? min(SEG, pos0 + r / G + 1 - key0) : 0;
       M[nt][i] = mk[nt][i] = -INFINITY;
       L[nt][i] = 0.0f;
       E[nt][i] = 0;
     }
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
+    o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.0f;
   }
 
   const auto wait_item = [&](int i) {
@@ -323,61 +325,61 @@ __global__ void __launch_bounds__(TH)
       ++issued;
     }
   };
-  const uint32_t ring = inv::smem_u32(sm.ring);
-  const uint32_t* qh32 = reinterpret_cast<const uint32_t*>(sm.qh);
-  const uint32_t* ql32 = reinterpret_cast<const uint32_t*>(sm.ql);
-  const uint32_t* wh32 = reinterpret_cast<const uint32_t*>(sm.wh);
-  const uint32_t* wl32 = reinterpret_cast<const uint32_t*>(sm.wl);
-  bool ok = true;
-
-  for (int b = 0; b < nblk; ++b) {
-    // ------------------------------------------------------------- scores --
-    ok = wait_item(2 * b) && ok;
-    float x[NT][2][4];  // keys 32 warp + 16 mt + g (+8), rows 2c, 2c + 1
-    {
-      const uint32_t kb = ring + ((2 * b) % NST) * SLOT;
+  // acc[nt] = sum over 16 x 8 codes of the m-tile at `ldsm(k)`: cross products first, then hi hi
+  const auto product = [&](const Frags* f, float (&acc)[NT][4], auto ldsm) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+    uint32_t ch[8][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt][mt][0] = x[nt][mt][1] = x[nt][mt][2] = x[nt][mt][3] = 0.0f;
-        const int lk = 32 * warp + 16 * mt + ((lane >> 3) & 1) * 8 + (lane & 7);
-        uint32_t ch[8][4];
+    for (int k = 0; k < 8; ++k) {
+      uint32_t w[4], cl[4];
+      ldsm(k, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t w[4], cl[4];
-          ldsm_x4(code_addr(kb, lk, 16 * k + (lane >> 4) * 8), w);
+      for (int i = 0; i < 4; ++i) inv::unpack_code(w[i], ch[k][i], cl[i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) inv::unpack_code(w[i], ch[k][i], cl[i]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int w0 = (8 * nt + g) * (PSTR / 2) + 8 * k + c;
-            mma16816(x[nt][mt], cl, qh32[w0], qh32[w0 + 4]);
-            mma16816(x[nt][mt], ch[k], ql32[w0], ql32[w0 + 4]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int w0 = (8 * nt + g) * (PSTR / 2) + 8 * k + c;
-            mma16816(x[nt][mt], ch[k], qh32[w0], qh32[w0 + 4]);
-          }
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0 && 8 * nt >= rows) break;
+        const uint4 b = f[nt].f[k][lane];
+        mma16816(acc[nt], cl, b.x, b.y);
+        mma16816(acc[nt], ch[k], b.z, b.w);
       }
     }
 #pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0 && 8 * nt >= rows) break;
+        const uint2 b = *reinterpret_cast<const uint2*>(&f[nt].f[k][lane]);
+        mma16816(acc[nt], ch[k], b.x, b.y);
+      }
+    }
+  };
+  const uint32_t ring = inv::smem_u32(sm.ring);
+  const int kk0 = 16 * warp + g;  // this lane's keys in a block: kk0, kk0 + 8
+  bool ok = true;
+
+#pragma unroll 1
+  for (int b = 0; b < nblk; ++b) {
+    // ------------------------------------------------------------- scores --
+    ok = wait_item(2 * b) && ok;
+    float x[NT][4];  // keys kk0 (+8), rows 2c, 2c + 1
+    {
+      const uint32_t kb = ring + ((2 * b) % NST) * SLOT;
+      product(sm.q, x, [&](int k, uint32_t (&w)[4]) {
+        ldsm_x4(code_addr(kb, 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), 16 * k + (lane >> 4) * 8), w);
+      });
+    }
+    const int key = b * BLK + kk0;
+    const float k0 = sm.ks[key], k1 = sm.ks[key + 8];
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = b * BLK + 32 * warp + 16 * mt + g + 8 * (i >> 1);
-          x[nt][mt][i] = key < nrow[nt][i & 1] ? __fmul_rn(x[nt][mt][i], sm.ks[key]) : -INFINITY;
-          mx[i & 1] = fmaxf(mx[i & 1], x[nt][mt][i]);
-        }
+      if (nt > 0 && 8 * nt >= rows) break;
+      float mx[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        x[nt][i] = key < nrow[nt][i] ? __fmul_rn(x[nt][i], k0) : -INFINITY;
+        x[nt][2 + i] = key + 8 < nrow[nt][i] ? __fmul_rn(x[nt][2 + i], k1) : -INFINITY;
+        mx[i] = fmaxf(x[nt][i], x[nt][2 + i]);
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 4));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 8));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 16));
@@ -390,50 +392,54 @@ __global__ void __launch_bounds__(TH)
 
     // ------------------------------------------------------------ softmax --
     float beta[NT][2];
+    const float v0 = sm.vs[key], v1 = sm.vs[key + 8];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float sc[2], ls[2];
-      const float m_old[2] = {mk[nt][0], mk[nt][1]};
+      if (nt > 0 && 8 * nt >= rows) break;
+      float2 mm = *reinterpret_cast<const float2*>(&sm.red_m[0][8 * nt + 2 * c]);
+#pragma unroll
+      for (int w = 1; w < FEW_WARPS; ++w) {
+        const float2 y = *reinterpret_cast<const float2*>(&sm.red_m[w][8 * nt + 2 * c]);
+        mm = make_float2(fmaxf(mm.x, y.x), fmaxf(mm.y, y.y));
+      }
+      __half* wf = reinterpret_cast<__half*>(&sm.w[nt].f[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = 8 * nt + 2 * c + i;
-        beta[nt][i] = 1.0f;
+        const float mk_old = mk[nt][i];
         const int seen = min(nrow[nt][i], (b + 1) * BLK);
+        beta[nt][i] = 1.0f;
         if (seen > b * BLK) {
-          const float m4 = fmaxf(fmaxf(sm.red_m[0][r], sm.red_m[1][r]), fmaxf(sm.red_m[2][r], sm.red_m[3][r]));
-          M[nt][i] = fmaxf(M[nt][i], m4);
+          M[nt][i] = fmaxf(M[nt][i], i == 0 ? mm.x : mm.y);
           mk[nt][i] = __fmul_rn(M[nt][i], kap[nt][i]);
           const int e_old = E[nt][i];
           E[nt][i] = inv::norm_exp(sm.pm[seen - 1]);
-          const float alpha = b == 0 ? 0.0f : inv::ex2(__fsub_rn(m_old[i], mk[nt][i]));
+          const float alpha = b == 0 ? 0.0f : inv::ex2(__fsub_rn(mk_old, mk[nt][i]));
           beta[nt][i] = b == 0 ? 0.0f : __fmul_rn(alpha, inv::pow2f(max(E[nt][i] - e_old, -126)));
           L[nt][i] = __fmul_rn(L[nt][i], alpha);
         }
-        sc[i] = inv::pow2f(E[nt][i]);
-        ls[i] = 0.0f;
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i & 1, kk = 32 * warp + 16 * mt + g + 8 * (i >> 1), key = b * BLK + kk;
-          float p = 0.0f, w = 0.0f;
-          if (key < nrow[nt][rr]) {
-            p = inv::ex2(__fmaf_rn(x[nt][mt][i], kap[nt][rr], -mk[nt][rr]));
-            w = __fmul_rn(p, __fmul_rn(sm.vs[key], sc[rr]));
-          }
-          ls[rr] = __fadd_rn(ls[rr], p);
-          __half hi, lo;
-          inv::split_plain(w, hi, lo);
-          sm.wh[(8 * nt + 2 * c + rr) * PSTR + kk] = hi;
-          sm.wl[(8 * nt + 2 * c + rr) * PSTR + kk] = lo;
+        const float sc = inv::pow2f(E[nt][i]);
+        float p0 = 0.0f, p1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
+        if (key < nrow[nt][i]) {
+          p0 = inv::ex2(__fmaf_rn(x[nt][i], kap[nt][i], -mk[nt][i]));
+          w0 = __fmul_rn(p0, __fmul_rn(v0, sc));
         }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ls[i] = __fadd_rn(ls[i], __shfl_xor_sync(0xffffffffu, ls[i], 4));
-        ls[i] = __fadd_rn(ls[i], __shfl_xor_sync(0xffffffffu, ls[i], 8));
-        ls[i] = __fadd_rn(ls[i], __shfl_xor_sync(0xffffffffu, ls[i], 16));
-        L[nt][i] = __fadd_rn(L[nt][i], ls[i]);
+        if (key + 8 < nrow[nt][i]) {
+          p1 = inv::ex2(__fmaf_rn(x[nt][2 + i], kap[nt][i], -mk[nt][i]));
+          w1 = __fmul_rn(p1, __fmul_rn(v1, sc));
+        }
+        __half h0, l0, h1, l1;
+        inv::split_plain(w0, h0, l0);
+        inv::split_plain(w1, h1, l1);
+        __half* d = wf + i * 32;  // row 2c + i: lane 4 (2c + i) + g / 2
+        d[0] = h0;
+        d[2] = h1;
+        d[4] = l0;
+        d[6] = l1;
+        float s = __fadd_rn(p0, p1);
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 8));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 16));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
+        L[nt][i] = __fadd_rn(L[nt][i], s);
       }
     }
     __syncthreads();
@@ -442,38 +448,14 @@ __global__ void __launch_bounds__(TH)
     ok = wait_item(2 * b + 1) && ok;
     {
       const uint32_t vb = ring + ((2 * b + 1) % NST) * SLOT;
+      product(sm.w, x, [&](int k, uint32_t (&w)[4]) {
+        ldsm_x4_t(code_addr(vb, 16 * k + (lane >> 4) * 8 + (lane & 7), 16 * warp + ((lane >> 3) & 1) * 8), w);
+      });
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        float acc[NT][4];
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0 && 8 * nt >= rows) break;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-        uint32_t ch[8][4];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t w[4], cl[4];
-          ldsm_x4_t(code_addr(vb, 16 * k + (lane >> 4) * 8 + (lane & 7), 32 * warp + 16 * mt + ((lane >> 3) & 1) * 8), w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) inv::unpack_code(w[i], ch[k][i], cl[i]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int w0 = (8 * nt + g) * (PSTR / 2) + 8 * k + c;
-            mma16816(acc[nt], cl, wh32[w0], wh32[w0 + 4]);
-            mma16816(acc[nt], ch[k], wl32[w0], wl32[w0 + 4]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int w0 = (8 * nt + g) * (PSTR / 2) + 8 * k + c;
-            mma16816(acc[nt], ch[k], wh32[w0], wh32[w0 + 4]);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (nrow[nt][i & 1] > b * BLK) o[nt][mt][i] = __fmaf_rn(o[nt][mt][i], beta[nt][i & 1], acc[nt][i]);
+        for (int i = 0; i < 4; ++i) o[nt][i] = __fmaf_rn(o[nt][i], beta[nt][i & 1], x[nt][i]);
       }
     }
     inv::fence_proxy_async_smem();  // V reads before the slot is overwritten
@@ -495,15 +477,13 @@ __global__ void __launch_bounds__(TH)
       const int64_t rs = part_index(a, t.seq, tok, t.row0 + tok, h * G + (r - tok * G)) + seg;
       if (!INV_IN_BOUNDS(a.status, rs, part_count(a))) continue;
       const float un = inv::pow2f(1 - E[nt][i]);
-      float* po = a.part_o + rs * D + 32 * warp + g;
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        po[16 * mt] = __fmul_rn(o[nt][mt][i], un);
-        po[16 * mt + 8] = __fmul_rn(o[nt][mt][2 + i], un);
-      }
+      float* po = a.part_o + rs * D + 16 * warp + g;
+      po[0] = __fmul_rn(o[nt][i], un);
+      po[8] = __fmul_rn(o[nt][2 + i], un);
       if (warp == 0 && g == 0) {
-        const float l = __fadd_rn(__fadd_rn(sm.red_l[0][r], sm.red_l[1][r]), __fadd_rn(sm.red_l[2][r], sm.red_l[3][r]));
-        a.part_ml[rs] = make_float2(mk[nt][i], l);
+        const float l0 = __fadd_rn(__fadd_rn(sm.red_l[0][r], sm.red_l[1][r]), __fadd_rn(sm.red_l[2][r], sm.red_l[3][r]));
+        const float l1 = __fadd_rn(__fadd_rn(sm.red_l[4][r], sm.red_l[5][r]), __fadd_rn(sm.red_l[6][r], sm.red_l[7][r]));
+        a.part_ml[rs] = make_float2(mk[nt][i], __fadd_rn(l0, l1));
       }
     }
   // no copy may still be landing when the CTA exits (only after a wait gave up)
@@ -679,11 +659,11 @@ __device__ __forceinline__ float score_max(uint32_t src, const float* ks, int nv
 }
 
 // Weights of 32 keys: replaces the scores at `src` by w as binary16, 16 columns
-// hi and 16 columns lo, and returns the sum of p (eight interleaved chains, then
-// a tree).  kFull: vs holds the scales times 2^E; else the raw ones, and only
+// hi and 16 columns lo, and returns the sums of p of either 16 keys (as the group
+// sums of the row arithmetic).  kFull: vs holds the scales times 2^E; else the raw ones, and only
 // the first nv keys have a weight.
 template <bool kFull>
-__device__ __forceinline__ float weights(uint32_t src, const float* ks, const float* vs, int nv, float kap, float mk,
+__device__ __forceinline__ float2 weights(uint32_t src, const float* ks, const float* vs, int nv, float kap, float mk,
                                          float vscale) {
   uint32_t v[32];
   tmem_ld32(src, v);
@@ -691,7 +671,7 @@ __device__ __forceinline__ float weights(uint32_t src, const float* ks, const fl
   const float4* k4 = reinterpret_cast<const float4*>(ks);
   const float4* v4 = reinterpret_cast<const float4*>(vs);
   const uint64_t kap2 = pk(kap, kap), mk2 = pk(-mk, -mk);
-  uint64_t s[4];
+  uint64_t s[8];
   uint32_t hi[16], lo[16];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -710,8 +690,8 @@ __device__ __forceinline__ float weights(uint32_t src, const float* ks, const fl
         uu[i] = mul2(uu[i], pk(vscale, vscale));
       }
       const uint64_t p = pk(pf.x, pf.y);
-      const int c = (2 * j + i) & 3;  // keys 2c, 2c + 1 of every 8
-      s[c] = e < 8 ? p : add2(s[c], p);
+      const int c = (e >> 4) * 4 + ((e >> 1) & 3);  // keys k, k + 1 of the first 8 of 16, with k + 8, k + 9
+      s[c] = (e & 8) == 0 ? p : add2(s[c], p);
       uint64_t w = mul2(p, uu[i]);
       if constexpr (!kFull) {  // (a scale behind the row's keys may overflow)
         const float2 wf = unpk(w);
@@ -722,9 +702,9 @@ __device__ __forceinline__ float weights(uint32_t src, const float* ks, const fl
   }
   tmem_st16(src, hi);
   tmem_st16(src + 16, lo);
-  const float2 a = unpk(s[0]), b = unpk(s[1]), c = unpk(s[2]), d = unpk(s[3]);
-  return __fadd_rn(__fadd_rn(__fadd_rn(a.x, a.y), __fadd_rn(b.x, b.y)),
-                   __fadd_rn(__fadd_rn(c.x, c.y), __fadd_rn(d.x, d.y)));
+  const float2 a = unpk(add2(add2(s[0], s[1]), add2(s[2], s[3])));
+  const float2 b = unpk(add2(add2(s[4], s[5]), add2(s[6], s[7])));
+  return make_float2(__fadd_rn(a.x, a.y), __fadd_rn(b.x, b.y));
 }
 
 [[maybe_unused]] __device__ __forceinline__ int64_t cache_rows(const AttnArgs& a) {
@@ -905,7 +885,8 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
     uint64_t O[32];  // the segment's sum, dims 64 hf + 2j, + 1
 #pragma unroll
     for (int j = 0; j < 32; ++j) O[j] = 0;
-    float M = -INFINITY, mk = -INFINITY, L0 = 0.0f, L1 = 0.0f;
+    float M = -INFINITY, mk = -INFINITY;
+    float L[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of the half's 16-key groups
     int E = 0;
     float Mt = -INFINITY, Lt = 0.0f;  // kDirect: folded segments
     float beta = 0.0f;                // of the block whose O is still to be added
@@ -942,20 +923,20 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
       const int E_s = E;
       float l_s = 0.0f;
       if (any || ends) {
-        const float lh = __fadd_rn(L0, L1);
+        const float lh = __fadd_rn(__fadd_rn(L[0], L[1]), __fadd_rn(L[2], L[3]));
         sm.red[exch & 1][hf][r] = make_float2(mx, lh);
         warp_arrive(&sm.row[warp & 3], lane);
         ok = bar_wait<true>(&sm.row[warp & 3], exch & 1, a, &sm.abort) && ok;
         const float2 other = sm.red[exch & 1][hf ^ 1][r];
         ++exch;
         mx = fmaxf(mx, other.x);
-        l_s = __fadd_rn(lh, other.y);  // (L_0 + L_1) + (L_2 + L_3) on either side
+        l_s = __fadd_rn(lh, other.y);
       }
       float beta_n = 1.0f;
       if (on) {
         if (first) {
           M = -INFINITY;
-          L0 = L1 = 0.0f;
+          L[0] = L[1] = L[2] = L[3] = 0.0f;
         }
         if (row_on) {
           M = fmaxf(M, mx);
@@ -963,25 +944,32 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
           E = inv::norm_exp(sm.pm[sl][min(BLK, nrow - b * BLK) - 1]);
           const float alpha = first ? 0.0f : inv::ex2(__fsub_rn(mk_s, mk));
           beta_n = first ? 0.0f : __fmul_rn(alpha, inv::pow2f(max(E - E_s, -126)));
-          L0 = __fmul_rn(L0, alpha);
-          L1 = __fmul_rn(L1, alpha);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) L[j] = __fmul_rn(L[j], alpha);
         }
-        float g = 0.0f;
+        float2 g = make_float2(0.0f, 0.0f);
         if (full) {
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
-            if (c != 0) L0 = __fadd_rn(L0, g);
+            if (c != 0) {
+              L[0] = __fadd_rn(L[0], g.x);
+              L[1] = __fadd_rn(L[1], g.y);
+            }
             g = weights<true>(sc + c, ks + c, sm.vs2[sl] + hf * 64 + c, 32, kap, mk, 1.0f);
           }
         } else if (any) {
           const float vscale = inv::pow2f(E);
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
-            if (c != 0) L0 = __fadd_rn(L0, g);
+            if (c != 0) {
+              L[0] = __fadd_rn(L[0], g.x);
+              L[1] = __fadd_rn(L[1], g.y);
+            }
             g = weights<false>(sc + c, ks + c, sm.vs[sl] + hf * 64 + c, nv - c, kap, mk, vscale);
           }
         }
-        L1 = __fadd_rn(L1, g);
+        L[2] = __fadd_rn(L[2], g.x);
+        L[3] = __fadd_rn(L[3], g.y);
         tmem_wait_st();
         inv::tc_fence_before();
         warp_arrive(&sm.p_full[i & 1], lane);
@@ -1430,9 +1418,9 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   if (rows <= 8)
     rc = launch_few<1, 3>(a, tk, tv, s);
   else if (rows <= 16)
-    rc = launch_few<2, 3>(a, tk, tv, s);
+    rc = launch_few<2, 2>(a, tk, tv, s);
   else
-    rc = launch_few<4, 3>(a, tk, tv, s);
+    rc = launch_few<4, 2>(a, tk, tv, s);
   if (rc == INV_OK && p.many) rc = p.direct ? launch_many<true>(a, s) : launch_many<false>(a, s);
   if (rc != INV_OK) return rc;
   return launch_fold(a, s);

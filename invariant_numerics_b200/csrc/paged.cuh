@@ -54,26 +54,30 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 // Two INT16 codes (low half first) as binary16 pairs with code / 2 = hi + lo,
 // hi = rn16(code / 2), both exact.  t = (code + 32768) >> 6 and l = code & 63
-// give code / 2 = 32 (t - 512) + l / 2 (1024 + t and 1024 + l are formed in the
-// binary16 mantissa); the sum rounds to hi and its error is lo.  (Keeping the
-// unrounded pair saves 3 of the 8 instructions, but then the dropped product
-// lo x_lo reaches 2^-20 of the row's largest code: 2.1e-6 against 8.6e-7 of
-// fp32 sums at 300 keys, where hi = rn16 leaves 2^-22 of each product.)
+// give code / 2 = 32 (t - 512) + l / 2; T = 1024 + t and U = 1024 + l are formed
+// in the binary16 mantissa.  With z = 32 T - 49664 = 32 (t - 512) - 512 (exact),
+// hi = rn16(U / 2 + z), and z - hi and lo = U / 2 + (z - hi) are exact again.
+// (Splitting into 32 (t - 512) and l / 2 saves two of the seven instructions,
+// but then the dropped product lo x_lo reaches 2^-20 of the row's largest code:
+// 2.1e-6 against 8.6e-7 of fp32 sums at 300 keys, where hi = rn16 leaves 2^-22
+// of each product.)
 __device__ __forceinline__ void unpack_code(uint32_t x, uint32_t& hi, uint32_t& lo) {
-  const uint32_t t = ((x >> 6) & 0x03FF03FFu) ^ 0x66006600u;  // 1024 + t (the xor biases the code)
-  const uint32_t l = (x & 0x003F003Fu) | 0x64006400u;         // 1024 + l
-  const uint32_t k32 = 0x50005000u, m49152 = 0xFA00FA00u;     // 32, -49152
-  const uint32_t kh = 0x38003800u, m512 = 0xE000E000u;        // 1/2, -512
-  const __half2 h0 = __hfma2(*reinterpret_cast<const __half2*>(&t), *reinterpret_cast<const __half2*>(&k32),
-                             *reinterpret_cast<const __half2*>(&m49152));
-  const __half2 l0 = __hfma2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&kh),
-                             *reinterpret_cast<const __half2*>(&m512));
-  const __half2 hv = __hadd2_rn(h0, l0);
-  const __half2 lv = __hadd2_rn(__hsub2_rn(h0, hv), l0);
-  hi = *reinterpret_cast<const uint32_t*>(&hv);
-  lo = *reinterpret_cast<const uint32_t*>(&lv);
+  uint32_t t, u;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(t) : "r"(x >> 6), "r"(0x03FF03FFu), "r"(0x66006600u));  // (a & b) ^ c
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(x), "r"(0x003F003Fu), "r"(0x64006400u));       // (a & b) | c
+  const uint32_t z = hfma2(t, 0x50005000u, 0xFA10FA10u);  // 32 T - 49664
+  hi = hfma2(u, 0x38003800u, z);                          // U / 2 + z
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(z), "r"(hi));
+  lo = hfma2(u, 0x38003800u, r);
 }
 
 // x = hi + lo up to 2^-22 |x| (not scaled: x is within a normalised range).
