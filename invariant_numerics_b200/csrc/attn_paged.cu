@@ -95,6 +95,17 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, int64_t idx, float
   }
 }
 
+__device__ __forceinline__ void store_out1(const AttnArgs& a, int64_t idx, float v) {
+  a.out[idx] = v;
+  if (a.out_hi) {
+    __half h, l;
+    inv::split_hi_lo(v, h, l);
+    if (inv::f16_overflow(v)) record_status(a.status, INV_ERR_RANGE);
+    a.out_hi[idx] = h;
+    a.out_lo[idx] = l;
+  }
+}
+
 // One tile of a sequence's new tokens.
 struct Tile {
   int seq, tok0, ntok;  // tokens tok0 .. tok0 + ntok - 1 of the sequence's new ones
@@ -139,16 +150,68 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, in
   return true;
 }
 
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(inv::smem_u32(bar)), "r"(parity), "r"(10000u)
+      : "memory");
+  return ok != 0;
+}
+// A wait that took long: true once it is to be given up.
+__device__ __forceinline__ bool wait_over(unsigned long long& t0, const AttnArgs& a, volatile int* abort) {
+  if (*abort) return true;
+  const unsigned long long now = inv::global_ns();
+  if (t0 == 0) t0 = now;
+  if ((long long)(now - t0) <= a.wait_ns) return false;
+  record_status(a.status, INV_ERR_TIMEOUT);
+  *abort = 1;
+  return true;
+}
+// mbar_wait by a whole warp (kWarp) or one thread, with polls that let the
+// hardware suspend it: the waiting warps share their schedulers with working
+// ones.  False once any wait of the CTA gave up.
+template <bool kWarp>
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, int* abort) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    const bool ok = mbar_poll(bar, parity);
+    if (kWarp ? __all_sync(0xffffffffu, ok) : ok) return true;
+    if ((i & 63u) == 0) {
+      const bool over = wait_over(t0, a, abort);
+      if (kWarp ? __any_sync(0xffffffffu, over) : over) return false;
+    }
+  }
+}
+
+// One arrival for the whole warp, behind all its lanes' accesses.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) inv::mbar_arrive(bar);
+}
+
 // ------------------------------------------------------- few rows: mma.sync --
 //
-// One CTA (8 warps) per (sequence of at most 8 NT rows, kv head, segment).  A
-// row is a (token, query head of the group) pair.  K and V blocks of 128 keys
-// stream through a ring of NST 32 KB slots (2-D TMA, 128-byte swizzle, one box
-// per page and half of d).  S^T = K Q^T: warp w owns keys 16w .. 16w+15 of the
-// block (the rows of an m-tile), the tile's rows are the MMA columns.  O^T = V^T
-// W: warp w owns dims 16w .. 16w+15.  W crosses the warps through shared memory.
-constexpr int TH = 256, FEW_WARPS = TH / 32;
+// Persistent CTAs (two a SM), each taking every gridDim.x-th work item = (sequence
+// of at most 8 NT rows, segment, kv head); a row is a (token, query head of the
+// group) pair.  Bound by HBM: 520 bytes a key and kv head.
+//   warp 8     producer: reads an item's descriptors and page numbers, brings its
+//              scales (bulk copies) and its K and V blocks of 128 keys (2-D TMA,
+//              128-byte swizzle, a box per page and half of d) into a ring of two
+//              32 KB slots, running ahead of the consumers across items, so that
+//              an item starts without waiting for memory (one CTA per item spent
+//              a quarter of its time there).
+//   warps 0-7  S^T = K Q^T: warp w owns keys 16w .. 16w+15 of the block (the rows
+//              of an m-tile), the item's rows are the MMA columns.  O^T = V^T W:
+//              warp w owns dims 16w .. 16w+15.  W crosses the warps through shared
+//              memory.
+constexpr int FEW_WARPS = 8, FEW_T = 32 * FEW_WARPS;
+constexpr int TH = FEW_T + 32;
 constexpr int SLOT = BLK * D * 2;  // 32 KB: codes of one block
+constexpr int NST = 2;
 
 // B fragments of 8 rows: lane (g, c) of k-step k holds, for row g, the pairs
 // (16k + 2c, + 1) and (16k + 2c + 8, + 9), hi and lo: {hi0, hi1, lo0, lo1}.
@@ -156,16 +219,23 @@ struct Frags {
   uint4 f[8][32];
 };
 
-template <int NT, int NST>
+// A work item; n_keys = 0: no more.
+struct Item {
+  int seq, row0, n_new, pos0, seg, h, n_keys;
+};
+
+template <int NT>
 struct __align__(1024) FewSmem {
   uint8_t ring[NST * SLOT];
   Frags q[NT], w[NT];
-  float ks[SEG], vs[SEG], pm[SEG];
+  float ks[2][SEG], vs[2][SEG];  // scales of this and the next item (unspecified behind their last key)
+  float pm[SEG];                 // running maximum of vs
   float red_m[FEW_WARPS][8 * NT];
   float red_l[FEW_WARPS][8 * NT];
   float kappa[8 * NT];
-  int pages[SEG / 16];
-  uint64_t full[NST];
+  int nrow[8 * NT];  // keys of the row in the segment (may be <= 0)
+  Item item[2];
+  uint64_t full[NST], empty[NST], item_full[2], item_empty[2];
   int abort;
 };
 
@@ -175,158 +245,133 @@ __device__ __forceinline__ uint32_t code_addr(uint32_t base, int r, int d0) {
   return base + (d0 >> 6) * (BLK * 128) + r * 128 + ((((d0 & 63) >> 3) ^ (r & 7)) << 4);
 }
 
-template <int NT, int NST>
+// Barrier of the consumer warps; true if `bad` holds for any of their threads.
+__device__ __forceinline__ bool few_sync_any(bool bad) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)bad), "n"(FEW_T)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void few_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(FEW_T) : "memory"); }
+
+// kLast: the fold is not launched (no sequence has a second segment); the item's
+// results are the rows' outputs.
+template <int NT, bool kLast>
 __global__ void __launch_bounds__(TH, 2)
     attn_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ AttnArgs a) {
   inv::grid_launch_dependents();  // the fold may be scheduled once every CTA has started
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int seg = blockIdx.x % a.S_max, h = blockIdx.y;
   const int G = a.G, Hkv = a.c.n_kv_heads;
-  Tile t;
-  if (!load_seq(a, blockIdx.x / a.S_max, lane, t) || t.n_new > a.few || t.n_new * G > 8 * NT) return;
-  const int rows = t.n_new * G;
-  const int pos0 = t.len - t.n_new;                // position of the first new token
-  const int key0 = seg * SEG, last = t.len;        // the rows see keys 0 .. last - 1 at most
-  if (key0 >= last) return;
-  const int n_keys = min(SEG, last - key0), nblk = (n_keys + BLK - 1) / BLK;
-
   extern __shared__ uint8_t smem_raw[];
-  using Smem = FewSmem<NT, NST>;
+  using Smem = FewSmem<NT>;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int sh = a.c.page_shift, ps = 1 << sh;
-
-  if (warp == 0) {
-    // page ids of the segment (a segment holds at most 32 pages)
-    const int npg = (n_keys + ps - 1) >> sh;
-    const int64_t e = (int64_t)(key0 >> sh) + lane;
-    int pg = 0;
-    if (lane < npg) {
-      pg = e < a.rb.ld_table ? a.rb.page_table[t.seq * a.rb.ld_table + e] : -1;
-      if (pg < 0 || pg >= a.c.n_pages) {
-        record_status(a.status, INV_ERR_INVALID_ARG);
-        pg = 0;
-      }
-    }
-    sm.pages[lane] = pg;
-    if (lane == 0) {
-      for (int i = 0; i < NST; ++i) inv::mbar_init(&sm.full[i], 1);
-      sm.abort = 0;
-      inv::fence_mbar_init();
-    }
-  }
-  __syncthreads();
-  // item 2b = K of block b, 2b + 1 = V of block b; item i lives in slot i % NST
-  const int items = 2 * nblk;
-  const auto issue = [&](int i) {  // one thread
-    const int b = i >> 1, s = i % NST;
-    const int kn = min(BLK, n_keys - b * BLK), box = min(ps, BLK), nb = (kn + box - 1) / box;
-    inv::mbar_arrive_expect_tx(&sm.full[s], nb * box * D * 2);
-    const CUtensorMap* tm = (i & 1) ? &tm_v : &tm_k;
-#pragma unroll 1
-    for (int j = 0; j < nb; ++j) {
-      const int kk = key0 + b * BLK + j * box;  // first key of the box
-      const int row = (sm.pages[(kk - key0) >> sh] * Hkv + h) * ps + (kk & (ps - 1));
-      uint8_t* dst = sm.ring + s * SLOT + j * box * 128;
-      inv::tma_load_2d(dst, tm, &sm.full[s], 0, row);
-      inv::tma_load_2d(dst + BLK * 128, tm, &sm.full[s], 64, row);
-    }
-  };
-  int issued = 0;
   if (tid == 0) {
-#pragma unroll 1
-    for (; issued < NST && issued < items; ++issued) issue(issued);
-  }
-
-  // scales of the segment (zero behind its last key), and their running maximum
-  {
-    float2 kv = make_float2(0.f, 0.f), vv = kv;
-    const int j = 2 * tid;  // keys j, j + 1: one page
-    if (j < n_keys) {
-      const int64_t row = ((int64_t)sm.pages[j >> sh] * Hkv + h) * ps + ((key0 + j) & (ps - 1));
-      if (INV_SPAN_IN_BOUNDS(a.status, row, row + 1, (int64_t)a.c.n_pages * Hkv * ps)) {
-        kv = *reinterpret_cast<const float2*>(a.c.k_scale + row);
-        vv = *reinterpret_cast<const float2*>(a.c.v_scale + row);
-      }
-      if (j + 1 >= n_keys) kv.y = vv.y = 0.0f;
+    for (int i = 0; i < NST; ++i) {
+      inv::mbar_init(&sm.full[i], 1);
+      inv::mbar_init(&sm.empty[i], FEW_WARPS);
     }
-    *reinterpret_cast<float2*>(sm.ks + j) = kv;
-    *reinterpret_cast<float2*>(sm.vs + j) = vv;
-    float up = fmaxf(vv.x, vv.y);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float x = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up = fmaxf(up, x);
+    for (int i = 0; i < 2; ++i) {
+      inv::mbar_init(&sm.item_full[i], 1);
+      inv::mbar_init(&sm.item_empty[i], FEW_WARPS);
     }
-    if (lane == 31) sm.red_m[0][warp] = up;  // (before red_m's first use)
-    float before = __shfl_up_sync(0xffffffffu, up, 1);
-    if (lane == 0) before = 0.0f;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before = fmaxf(before, sm.red_m[0][w]);
-    const float p0 = fmaxf(before, vv.x);
-    *reinterpret_cast<float2*>(sm.pm + j) = make_float2(p0, fmaxf(p0, vv.y));
-  }
-  // the rows' q, scaled by 2^e and split; lane holds dims 4 lane .. 4 lane + 3
-#pragma unroll 1
-  for (int r = warp; r < 8 * NT; r += FEW_WARPS) {
-    const int tok = r / G, head = r - tok * G;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
-      const int64_t iq = (int64_t)(t.row0 + tok) * a.ld_q + (int64_t)(h * G + head) * D;
-      if (INV_SPAN_IN_BOUNDS(a.status, iq, iq + D - 1, (int64_t)(a.T - 1) * a.ld_q + (int64_t)a.Hq * D))
-        x = reinterpret_cast<const float4*>(a.q + iq)[lane];
-    }
-    float m = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int e = inv::norm_exp(m);
-    const float f = inv::pow2f(e);
-    __half hi[4], lo[4];
-    inv::split_plain(__fmul_rn(x.x, f), hi[0], lo[0]);
-    inv::split_plain(__fmul_rn(x.y, f), hi[1], lo[1]);
-    inv::split_plain(__fmul_rn(x.z, f), hi[2], lo[2]);
-    inv::split_plain(__fmul_rn(x.w, f), hi[3], lo[3]);
-    // dims 4 lane, + 1 and + 2, + 3: k-step lane / 4, pair of c = 2 (lane % 2), + 1 of its half (lane % 4) / 2
-    uint32_t* dst = reinterpret_cast<uint32_t*>(&sm.q[r >> 3].f[lane >> 2][4 * (r & 7) + 2 * (lane & 1)]) + ((lane >> 1) & 1);
-    dst[0] = pack_half2(hi[0], hi[1]);
-    dst[2] = pack_half2(lo[0], lo[1]);
-    dst[4] = pack_half2(hi[2], hi[3]);
-    dst[6] = pack_half2(lo[2], lo[3]);
-    if (lane == 0) sm.kappa[r] = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
+    sm.abort = 0;
+    inv::fence_mbar_init();
   }
   __syncthreads();
+  bool ok = true;
 
-  // state of the rows 2c, 2c + 1 of every n-tile (the same in all lanes and warps that share c; L is the warp's)
-  float kap[NT][2], M[NT][2], mk[NT][2], L[NT][2];
-  int E[NT][2], nrow[NT][2];  // nrow: keys of the row in the segment
-  float o[NT][4];             // O of dims 16 warp + g (+8), rows 2c, 2c + 1
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * nt + 2 * c + i;
-      kap[nt][i] = sm.kappa[r];
-      nrow[nt][i] = r < rows ? min(SEG, pos0 + r / G + 1 - key0) : 0;
-      M[nt][i] = mk[nt][i] = -INFINITY;
-      L[nt][i] = 0.0f;
-      E[nt][i] = 0;
+  if (warp == FEW_WARPS) {
+    // =============================================================== producer
+    const int sh = a.c.page_shift, ps = 1 << sh, box = min(ps, BLK);
+    const int64_t items = (int64_t)a.rb.n_seqs * a.S_max * Hkv;
+    uint32_t n_item = 0, n_slot = 0;  // items and blocks sent so far
+#pragma unroll 1
+    for (int64_t id = blockIdx.x; id < items && ok; id += gridDim.x) {
+      Item it;
+      it.h = (int)(id % Hkv);
+      const int64_t rest = id / Hkv;
+      it.seg = (int)(rest % a.S_max);
+      Tile t;
+      if (!load_seq(a, (int)(rest / a.S_max), lane, t) || t.n_new > a.few || t.n_new * G > 8 * NT) continue;
+      const int key0 = it.seg * SEG;
+      it.seq = t.seq;
+      it.row0 = t.row0;
+      it.n_new = t.n_new;
+      it.pos0 = t.len - t.n_new;
+      it.n_keys = min(SEG, t.len - key0);
+      if (it.n_keys <= 0) continue;
+      // lane j: page j of the segment (at most 32), as the cache row of this head's first key
+      const int npg = (it.n_keys + ps - 1) >> sh;
+      int row = 0;
+      if (lane < npg) {
+        int pg = a.rb.page_table[t.seq * a.rb.ld_table + (key0 >> sh) + lane];
+        if (pg < 0 || pg >= a.c.n_pages) {
+          record_status(a.status, INV_ERR_INVALID_ARG);
+          pg = 0;
+        }
+        row = (pg * Hkv + it.h) << sh;
+      }
+      const int ab = n_item & 1;
+      if (n_item >= 2) ok = bar_wait<true>(&sm.item_empty[ab], ((n_item >> 1) - 1) & 1, a, &sm.abort) && ok;
+      if (!ok) break;
+      if (lane == 0) {
+        sm.item[ab] = it;
+        inv::mbar_arrive_expect_tx(&sm.item_full[ab], npg * ps * 8);
+      }
+      __syncwarp();
+      if (lane < npg && INV_SPAN_IN_BOUNDS(a.status, row, row + ps - 1, ((int64_t)a.c.n_pages * Hkv) << sh)) {
+        inv::bulk_load(sm.ks[ab] + (lane << sh), a.c.k_scale + row, ps * 4, &sm.item_full[ab]);
+        inv::bulk_load(sm.vs[ab] + (lane << sh), a.c.v_scale + row, ps * 4, &sm.item_full[ab]);
+      }
+      ++n_item;
+      const int ops = 2 * ((it.n_keys + BLK - 1) / BLK);  // K, V of every block
+#pragma unroll 1
+      for (int op = 0; op < ops && ok; ++op) {
+        const int s = n_slot % NST;
+        if (n_slot >= NST) ok = bar_wait<true>(&sm.empty[s], (n_slot / NST - 1) & 1, a, &sm.abort) && ok;
+        if (!ok) break;
+        const int kb = (op >> 1) * BLK, nb = (min(BLK, it.n_keys - kb) + box - 1) / box;
+        if (lane == 0) inv::mbar_arrive_expect_tx(&sm.full[s], nb * box * D * 2);
+        __syncwarp();
+        // lane j: box j (keys kb + j box ..): both halves of d
+        const int kk = kb + lane * box;
+        const int r0 = __shfl_sync(0xffffffffu, row, (kk >> sh) & 31);
+        if (lane < nb) {
+          const CUtensorMap* tm = (op & 1) ? &tm_v : &tm_k;
+          uint8_t* dst = sm.ring + s * SLOT + lane * box * 128;
+          inv::tma_load_2d(dst, tm, &sm.full[s], 0, r0 + (kk & (ps - 1)));
+          inv::tma_load_2d(dst + BLK * 128, tm, &sm.full[s], 64, r0 + (kk & (ps - 1)));
+        }
+        ++n_slot;
+      }
     }
-    o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.0f;
+    // the end mark; after a wait that gave up, no copy may still be landing when the CTA exits
+    const int ab = n_item & 1;
+    if (ok && n_item >= 2) ok = bar_wait<true>(&sm.item_empty[ab], ((n_item >> 1) - 1) & 1, a, &sm.abort);
+    if (ok) {
+      if (lane == 0) {
+        sm.item[ab].n_keys = 0;
+        inv::mbar_arrive(&sm.item_full[ab]);
+      }
+    } else if (lane == 0) {
+      for (uint32_t i = n_slot > NST ? n_slot - NST : 0; i < n_slot; ++i)
+        inv::mbar_wait(&sm.full[i % NST], (i / NST) & 1, a.wait_ns, nullptr, a.status);
+      for (uint32_t i = n_item > 2 ? n_item - 2 : 0; i < n_item; ++i)
+        inv::mbar_wait(&sm.item_full[i & 1], (i >> 1) & 1, a.wait_ns, nullptr, a.status);
+    }
+    return;
   }
 
-  const auto wait_item = [&](int i) {
-    bool ok = true;
-    if (lane == 0) ok = inv::mbar_wait(&sm.full[i % NST], (i / NST) & 1, a.wait_ns, &sm.abort, a.status);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-  };
-  const auto refill = [&]() {  // thread 0, after a barrier behind the last reads of the oldest slot
-    if (tid == 0 && issued < items && !sm.abort) {
-      issue(issued);
-      ++issued;
-    }
-  };
+  // ================================================================ consumers
   // acc[nt] = sum over 16 x 8 codes of the m-tile at `ldsm(k)`: cross products first, then hi hi
-  const auto product = [&](const Frags* f, float (&acc)[NT][4], auto ldsm) {
+  const auto product = [&](int rows, const Frags* f, float (&acc)[NT][4], auto ldsm) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
     uint32_t ch[8][4];
@@ -356,140 +401,241 @@ __global__ void __launch_bounds__(TH, 2)
   };
   const uint32_t ring = inv::smem_u32(sm.ring);
   const int kk0 = 16 * warp + g;  // this lane's keys in a block: kk0, kk0 + 8
-  bool ok = true;
+  uint32_t n_slot = 0;
 
 #pragma unroll 1
-  for (int b = 0; b < nblk; ++b) {
-    // ------------------------------------------------------------- scores --
-    ok = wait_item(2 * b) && ok;
-    float x[NT][4];  // keys kk0 (+8), rows 2c, 2c + 1
-    {
-      const uint32_t kb = ring + ((2 * b) % NST) * SLOT;
-      product(sm.q, x, [&](int k, uint32_t (&w)[4]) {
-        ldsm_x4(code_addr(kb, 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), 16 * k + (lane >> 4) * 8), w);
-      });
+  for (uint32_t n_item = 0;; ++n_item) {
+    const int ab = n_item & 1;
+    ok = bar_wait<true>(&sm.item_full[ab], (n_item >> 1) & 1, a, &sm.abort) && ok;
+    if (few_sync_any(!ok)) break;
+    const Item it = sm.item[ab];
+    if (it.n_keys == 0) break;
+    const int rows = it.n_new * G, key0 = it.seg * SEG, nblk = (it.n_keys + BLK - 1) / BLK;
+    const float* ks = sm.ks[ab];
+    const float* vs = sm.vs[ab];
+    // the rows' q, scaled by 2^e and split; lane holds dims 4 lane .. 4 lane + 3
+    float4 qx[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int r = warp + FEW_WARPS * i, tok = r / G;
+      qx[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        const int64_t iq = (int64_t)(it.row0 + tok) * a.ld_q + (int64_t)(it.h * G + r - tok * G) * D;
+        if (INV_SPAN_IN_BOUNDS(a.status, iq, iq + D - 1, (int64_t)(a.T - 1) * a.ld_q + (int64_t)a.Hq * D))
+          qx[i] = reinterpret_cast<const float4*>(a.q + iq)[lane];
+      }
     }
-    const int key = b * BLK + kk0;
-    const float k0 = sm.ks[key], k1 = sm.ks[key + 8];
+    {
+      // running maximum of the V scales: keys 2 tid, 2 tid + 1
+      const int j = 2 * tid;
+      const float s0 = j < it.n_keys ? vs[j] : 0.0f, s1 = j + 1 < it.n_keys ? vs[j + 1] : 0.0f;
+      float up = fmaxf(s0, s1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up = fmaxf(up, x);
+      }
+      if (lane == 31) sm.red_m[0][warp] = up;  // (before red_m's first use)
+      float before = __shfl_up_sync(0xffffffffu, up, 1);
+      if (lane == 0) before = 0.0f;
+      few_sync();
+      for (int w = 0; w < warp; ++w) before = fmaxf(before, sm.red_m[0][w]);
+      const float p0 = fmaxf(before, s0);
+      *reinterpret_cast<float2*>(sm.pm + j) = make_float2(p0, fmaxf(p0, s1));
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int r = warp + FEW_WARPS * i;
+      const float4 x = qx[i];
+      float m = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int e = inv::norm_exp(m);
+      const float f = inv::pow2f(e);
+      __half hi[4], lo[4];
+      inv::split_plain(__fmul_rn(x.x, f), hi[0], lo[0]);
+      inv::split_plain(__fmul_rn(x.y, f), hi[1], lo[1]);
+      inv::split_plain(__fmul_rn(x.z, f), hi[2], lo[2]);
+      inv::split_plain(__fmul_rn(x.w, f), hi[3], lo[3]);
+      // dims 4 lane, + 1 and + 2, + 3: k-step lane / 4, pairs c = 2 (lane % 2), + 1 of its half (lane % 4) / 2
+      uint32_t* dst = reinterpret_cast<uint32_t*>(&sm.q[r >> 3].f[lane >> 2][4 * (r & 7) + 2 * (lane & 1)]) + ((lane >> 1) & 1);
+      dst[0] = pack_half2(hi[0], hi[1]);
+      dst[2] = pack_half2(lo[0], lo[1]);
+      dst[4] = pack_half2(hi[2], hi[3]);
+      dst[6] = pack_half2(lo[2], lo[3]);
+      if (lane == 0) {
+        sm.kappa[r] = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
+        sm.nrow[r] = r < rows ? min(SEG, it.pos0 + r / G + 1 - key0) : 0;
+      }
+    }
+    few_sync();
+
+    // lane r of every warp keeps the state of row r; L and O are per thread: L of rows 2c, 2c + 1 of every n-tile over
+    // the warp's keys (the same in all lanes that share c), O of these rows, dims 16 warp + g (+8)
+    const int nrow_r = lane < 8 * NT ? sm.nrow[lane & (8 * NT - 1)] : 0;
+    const float kap_r = lane < 8 * NT ? sm.kappa[lane & (8 * NT - 1)] : 0.0f;
+    float M_r = -INFINITY, mk_r = -INFINITY;
+    int E_r = 0;
+    float L[NT][2], o[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0 && 8 * nt >= rows) break;
-      float mx[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[nt][i] = key < nrow[nt][i] ? __fmul_rn(x[nt][i], k0) : -INFINITY;
-        x[nt][2 + i] = key + 8 < nrow[nt][i] ? __fmul_rn(x[nt][2 + i], k1) : -INFINITY;
-        mx[i] = fmaxf(x[nt][i], x[nt][2 + i]);
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 4));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 8));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 16));
-      }
-      if (g == 0) *reinterpret_cast<float2*>(&sm.red_m[warp][8 * nt + 2 * c]) = make_float2(mx[0], mx[1]);
+      L[nt][0] = L[nt][1] = 0.0f;
+      o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.0f;
     }
-    inv::fence_proxy_async_smem();  // this thread's K reads before the TMA overwrites the slot
-    __syncthreads();
-    refill();
 
-    // ------------------------------------------------------------ softmax --
-    float beta[NT][2];
-    const float v0 = sm.vs[key], v1 = sm.vs[key + 8];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0 && 8 * nt >= rows) break;
-      float2 mm = *reinterpret_cast<const float2*>(&sm.red_m[0][8 * nt + 2 * c]);
-#pragma unroll
-      for (int w = 1; w < FEW_WARPS; ++w) {
-        const float2 y = *reinterpret_cast<const float2*>(&sm.red_m[w][8 * nt + 2 * c]);
-        mm = make_float2(fmaxf(mm.x, y.x), fmaxf(mm.y, y.y));
+    bool gone = false;
+#pragma unroll 1
+    for (int b = 0; b < nblk; ++b) {
+      // ----------------------------------------------------------- scores --
+      ok = bar_wait<true>(&sm.full[n_slot % NST], (n_slot / NST) & 1, a, &sm.abort) && ok;
+      float x[NT][4];  // keys kk0 (+8), rows 2c, 2c + 1
+      {
+        const uint32_t kb = ring + (n_slot % NST) * SLOT;
+        product(rows, sm.q, x, [&](int k, uint32_t (&w)[4]) {
+          ldsm_x4(code_addr(kb, 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), 16 * k + (lane >> 4) * 8), w);
+        });
       }
-      __half* wf = reinterpret_cast<__half*>(&sm.w[nt].f[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float mk_old = mk[nt][i];
-        const int seen = min(nrow[nt][i], (b + 1) * BLK);
-        beta[nt][i] = 1.0f;
-        if (seen > b * BLK) {
-          M[nt][i] = fmaxf(M[nt][i], i == 0 ? mm.x : mm.y);
-          mk[nt][i] = __fmul_rn(M[nt][i], kap[nt][i]);
-          const int e_old = E[nt][i];
-          E[nt][i] = inv::norm_exp(sm.pm[seen - 1]);
-          const float alpha = b == 0 ? 0.0f : inv::ex2(__fsub_rn(mk_old, mk[nt][i]));
-          beta[nt][i] = b == 0 ? 0.0f : __fmul_rn(alpha, inv::pow2f(max(E[nt][i] - e_old, -126)));
-          L[nt][i] = __fmul_rn(L[nt][i], alpha);
-        }
-        const float sc = inv::pow2f(E[nt][i]);
-        float p0 = 0.0f, p1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
-        if (key < nrow[nt][i]) {
-          p0 = inv::ex2(__fmaf_rn(x[nt][i], kap[nt][i], -mk[nt][i]));
-          w0 = __fmul_rn(p0, __fmul_rn(v0, sc));
-        }
-        if (key + 8 < nrow[nt][i]) {
-          p1 = inv::ex2(__fmaf_rn(x[nt][2 + i], kap[nt][i], -mk[nt][i]));
-          w1 = __fmul_rn(p1, __fmul_rn(v1, sc));
-        }
-        __half h0, l0, h1, l1;
-        inv::split_plain(w0, h0, l0);
-        inv::split_plain(w1, h1, l1);
-        __half* d = wf + i * 32;  // row 2c + i: lane 4 (2c + i) + g / 2
-        d[0] = h0;
-        d[2] = h1;
-        d[4] = l0;
-        d[6] = l1;
-        float s = __fadd_rn(p0, p1);
-        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 8));
-        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 16));
-        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
-        L[nt][i] = __fadd_rn(L[nt][i], s);
-      }
-    }
-    __syncthreads();
-
-    // ------------------------------------------------------------- values --
-    ok = wait_item(2 * b + 1) && ok;
-    {
-      const uint32_t vb = ring + ((2 * b + 1) % NST) * SLOT;
-      product(sm.w, x, [&](int k, uint32_t (&w)[4]) {
-        ldsm_x4_t(code_addr(vb, 16 * k + (lane >> 4) * 8 + (lane & 7), 16 * warp + ((lane >> 3) & 1) * 8), w);
-      });
+      inv::fence_proxy_async_smem();  // the slot's reads before the TMA overwrites it
+      warp_arrive(&sm.empty[n_slot % NST], lane);
+      ++n_slot;
+      const int key = b * BLK + kk0;
+      const float k0 = ks[key], k1 = ks[key + 8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt > 0 && 8 * nt >= rows) break;
+        float mx[2];
+        const int2 nr = *reinterpret_cast<const int2*>(&sm.nrow[8 * nt + 2 * c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[nt][i] = __fmaf_rn(o[nt][i], beta[nt][i & 1], x[nt][i]);
+        for (int i = 0; i < 2; ++i) {
+          const int nri = i == 0 ? nr.x : nr.y;
+          x[nt][i] = key < nri ? __fmul_rn(x[nt][i], k0) : -INFINITY;
+          x[nt][2 + i] = key + 8 < nri ? __fmul_rn(x[nt][2 + i], k1) : -INFINITY;
+          mx[i] = fmaxf(x[nt][i], x[nt][2 + i]);
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 4));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 8));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 16));
+        }
+        if (g == 0) *reinterpret_cast<float2*>(&sm.red_m[warp][8 * nt + 2 * c]) = make_float2(mx[0], mx[1]);
       }
-    }
-    inv::fence_proxy_async_smem();  // V reads before the slot is overwritten
-    __syncthreads();
-    refill();
-  }
+      if (few_sync_any(!ok)) {  // (also: every warp has read the previous block's W)
+        gone = true;
+        break;
+      }
 
-  // -------------------------------------------------------- segment results --
+      // ---------------------------------------------------------- softmax --
+      float alpha_r = 1.0f, beta_r = 1.0f;
+      {
+        const int seen = min(nrow_r, (b + 1) * BLK);
+        if (seen > b * BLK) {
+          float m = sm.red_m[0][lane & (8 * NT - 1)];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-    if (g == 0) *reinterpret_cast<float2*>(&sm.red_l[warp][8 * nt + 2 * c]) = make_float2(L[nt][0], L[nt][1]);
-  __syncthreads();
+          for (int w = 1; w < FEW_WARPS; ++w) m = fmaxf(m, sm.red_m[w][lane & (8 * NT - 1)]);
+          M_r = fmaxf(M_r, m);
+          const float mk_old = mk_r;
+          const int e_old = E_r;
+          mk_r = __fmul_rn(M_r, kap_r);
+          E_r = inv::norm_exp(sm.pm[seen - 1]);
+          alpha_r = b == 0 ? 0.0f : inv::ex2(__fsub_rn(mk_old, mk_r));
+          beta_r = b == 0 ? 0.0f : __fmul_rn(alpha_r, inv::pow2f(max(E_r - e_old, -126)));
+        }
+      }
+      const float v0 = vs[key], v1 = vs[key + 8];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0 && 8 * nt >= rows) break;
+        const float2 kap2 = *reinterpret_cast<const float2*>(&sm.kappa[8 * nt + 2 * c]);
+        __half* wf = reinterpret_cast<__half*>(&sm.w[nt].f[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * nt + 2 * c + i, tok = r / G;
-      if (!ok || nrow[nt][i] <= 0) continue;
-      const int64_t rs = part_index(a, t.seq, tok, t.row0 + tok, h * G + (r - tok * G)) + seg;
-      if (!INV_IN_BOUNDS(a.status, rs, part_count(a))) continue;
-      const float un = inv::pow2f(1 - E[nt][i]);
-      float* po = a.part_o + rs * D + 16 * warp + g;
-      po[0] = __fmul_rn(o[nt][i], un);
-      po[8] = __fmul_rn(o[nt][2 + i], un);
-      if (warp == 0 && g == 0) {
+        for (int i = 0; i < 2; ++i) {
+          const int src = 8 * nt + 2 * c + i;
+          const float kap = i == 0 ? kap2.x : kap2.y, mk = __shfl_sync(0xffffffffu, mk_r, src);
+          const float sc = inv::pow2f(__shfl_sync(0xffffffffu, E_r, src));
+          L[nt][i] = __fmul_rn(L[nt][i], __shfl_sync(0xffffffffu, alpha_r, src));
+          // (a key the row does not see has x = -inf: p = 0)
+          float p0 = 0.0f, p1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
+          if (x[nt][i] != -INFINITY) {
+            p0 = inv::ex2(__fmaf_rn(x[nt][i], kap, -mk));
+            w0 = __fmul_rn(p0, __fmul_rn(v0, sc));
+          }
+          if (x[nt][2 + i] != -INFINITY) {
+            p1 = inv::ex2(__fmaf_rn(x[nt][2 + i], kap, -mk));
+            w1 = __fmul_rn(p1, __fmul_rn(v1, sc));
+          }
+          __half h0, l0, h1, l1;
+          inv::split_plain(w0, h0, l0);
+          inv::split_plain(w1, h1, l1);
+          __half* d = wf + i * 32;  // row 2c + i: lane 4 (2c + i) + g / 2
+          d[0] = h0;
+          d[2] = h1;
+          d[4] = l0;
+          d[6] = l1;
+          float s = __fadd_rn(p0, p1);
+          s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 8));
+          s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 16));
+          s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
+          L[nt][i] = __fadd_rn(L[nt][i], s);
+        }
+      }
+      few_sync();
+
+      // ----------------------------------------------------------- values --
+      ok = bar_wait<true>(&sm.full[n_slot % NST], (n_slot / NST) & 1, a, &sm.abort) && ok;
+      {
+        const uint32_t vb = ring + (n_slot % NST) * SLOT;
+        product(rows, sm.w, x, [&](int k, uint32_t (&w)[4]) {
+          ldsm_x4_t(code_addr(vb, 16 * k + (lane >> 4) * 8 + (lane & 7), 16 * warp + ((lane >> 3) & 1) * 8), w);
+        });
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (nt > 0 && 8 * nt >= rows) break;
+          const float b0 = __shfl_sync(0xffffffffu, beta_r, 8 * nt + 2 * c), b1 = __shfl_sync(0xffffffffu, beta_r, 8 * nt + 2 * c + 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nt][i] = __fmaf_rn(o[nt][i], (i & 1) ? b1 : b0, x[nt][i]);
+        }
+      }
+      inv::fence_proxy_async_smem();
+      warp_arrive(&sm.empty[n_slot % NST], lane);
+      ++n_slot;
+    }
+    if (gone) break;
+
+    // ------------------------------------------------------ segment results --
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (g == 0) *reinterpret_cast<float2*>(&sm.red_l[warp][8 * nt + 2 * c]) = make_float2(L[nt][0], L[nt][1]);
+    inv::fence_proxy_async_smem();  // the scales' reads before the next copy into their buffer
+    warp_arrive(&sm.item_empty[ab], lane);
+    few_sync();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * nt + 2 * c + i, tok = r / G, head = it.h * G + (r - tok * G);
+        const int E = __shfl_sync(0xffffffffu, E_r, r);
+        const float mk = __shfl_sync(0xffffffffu, mk_r, r);
+        if (!ok || sm.nrow[r] <= 0) continue;
+        const float un = inv::pow2f(1 - E);
+        const float y0 = __fmul_rn(o[nt][i], un), y1 = __fmul_rn(o[nt][2 + i], un);
         const float l0 = __fadd_rn(__fadd_rn(sm.red_l[0][r], sm.red_l[1][r]), __fadd_rn(sm.red_l[2][r], sm.red_l[3][r]));
         const float l1 = __fadd_rn(__fadd_rn(sm.red_l[4][r], sm.red_l[5][r]), __fadd_rn(sm.red_l[6][r], sm.red_l[7][r]));
-        a.part_ml[rs] = make_float2(mk[nt][i], __fadd_rn(l0, l1));
+        const float l = __fadd_rn(l0, l1);
+        if constexpr (kLast) {
+          // the fold of one segment: its factor is 1
+          const int64_t io = ((int64_t)(it.row0 + tok) * a.Hq + head) * D + 16 * warp + g;
+          if (!INV_SPAN_IN_BOUNDS(a.status, io, io + 8, (int64_t)a.T * a.Hq * D)) continue;
+          const float il = __frcp_rn(l);
+          store_out1(a, io, __fmul_rn(y0, il));
+          store_out1(a, io + 8, __fmul_rn(y1, il));
+        } else {
+          const int64_t rs = part_index(a, it.seq, tok, it.row0 + tok, head) + it.seg;
+          if (!INV_IN_BOUNDS(a.status, rs, part_count(a))) continue;
+          float* po = a.part_o + rs * D + 16 * warp + g;
+          po[0] = y0;
+          po[8] = y1;
+          if (warp == 0 && g == 0) a.part_ml[rs] = make_float2(mk, l);
+        }
       }
-    }
-  // no copy may still be landing when the CTA exits (only after a wait gave up)
-  if (!ok && tid == 0)
-    for (int i = max(0, issued - NST); i < issued; ++i)
-      inv::mbar_wait(&sm.full[i % NST], (i / NST) & 1, a.wait_ns, nullptr, a.status);
+  }
 }
 
 // --------------------------------------------------------- many rows: tcgen05 --
@@ -721,49 +867,6 @@ __device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int seq, int h, 
     return -1;
   }
   return (((int64_t)pg * a.c.n_kv_heads + h) << sh) + (key & ((1 << sh) - 1));
-}
-
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(inv::smem_u32(bar)), "r"(parity), "r"(10000u)
-      : "memory");
-  return ok != 0;
-}
-// A wait that took long: true once it is to be given up.
-__device__ __forceinline__ bool wait_over(unsigned long long& t0, const AttnArgs& a, volatile int* abort) {
-  if (*abort) return true;
-  const unsigned long long now = inv::global_ns();
-  if (t0 == 0) t0 = now;
-  if ((long long)(now - t0) <= a.wait_ns) return false;
-  record_status(a.status, INV_ERR_TIMEOUT);
-  *abort = 1;
-  return true;
-}
-// mbar_wait by a whole warp (kWarp) or one thread, with polls that let the
-// hardware suspend it: the waiting warps share their schedulers with working
-// ones.  False once any wait of the CTA gave up.
-template <bool kWarp>
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const AttnArgs& a, int* abort) {
-  unsigned long long t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    const bool ok = mbar_poll(bar, parity);
-    if (kWarp ? __all_sync(0xffffffffu, ok) : ok) return true;
-    if ((i & 63u) == 0) {
-      const bool over = wait_over(t0, a, abort);
-      if (kWarp ? __any_sync(0xffffffffu, over) : over) return false;
-    }
-  }
-}
-
-// One arrival for the whole warp, behind all its lanes' accesses.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  __syncwarp();
-  if (lane == 0) inv::mbar_arrive(bar);
 }
 
 // One lane of the warp (a branch on it leaves the MMA operands in uniform
@@ -1288,7 +1391,10 @@ struct Plan {
 Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
   const int G = Hq / Hkv, S = segments(max_len), few = few_tokens(G);
   Plan p = {max_q > few, false, 1, (int64_t)T * Hq};
-  if (!p.many) return p;
+  if (!p.many) {
+    if (S == 1) p.parts = 0;
+    return p;
+  }
   const int64_t ctas = ((int64_t)T / (MANY_ROWS / G) + 1) * Hkv;
   p.direct = ctas >= 2 * inv::sm_count() || S == 1;
   if (p.direct) {
@@ -1298,13 +1404,14 @@ Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
   return p;
 }
 
-template <int NT, int NST>
+template <int NT, bool kLast>
 int launch_few(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   static bool done[64] = {};
-  constexpr size_t smem = sizeof(FewSmem<NT, NST>) + 1024;
-  const int rc = allow_smem(attn_few_kernel<NT, NST>, smem, done);
+  constexpr size_t smem = sizeof(FewSmem<NT>) + 1024;
+  const int rc = allow_smem(attn_few_kernel<NT, kLast>, smem, done);
   if (rc != INV_OK) return rc;
-  attn_few_kernel<NT, NST><<<dim3((unsigned)(a.rb.n_seqs * a.S_max), a.c.n_kv_heads), TH, smem, s>>>(tk, tv, a);
+  const int64_t items = (int64_t)a.rb.n_seqs * a.S_max * a.c.n_kv_heads, fit = 2 * inv::sm_count();
+  attn_few_kernel<NT, kLast><<<(unsigned)(items < fit ? items : fit), TH, smem, s>>>(tk, tv, a);
   INV_CHECK_LAUNCH();
   return INV_OK;
 }
@@ -1415,15 +1522,16 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   if (rc != INV_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rows = (a.max_q < a.few ? a.max_q : a.few) * G;
+  const bool last = !p.many && a.S_max == 1;  // no fold
   if (rows <= 8)
-    rc = launch_few<1, 3>(a, tk, tv, s);
+    rc = last ? launch_few<1, true>(a, tk, tv, s) : launch_few<1, false>(a, tk, tv, s);
   else if (rows <= 16)
-    rc = launch_few<2, 2>(a, tk, tv, s);
+    rc = last ? launch_few<2, true>(a, tk, tv, s) : launch_few<2, false>(a, tk, tv, s);
   else
-    rc = launch_few<4, 2>(a, tk, tv, s);
+    rc = last ? launch_few<4, true>(a, tk, tv, s) : launch_few<4, false>(a, tk, tv, s);
   if (rc == INV_OK && p.many) rc = p.direct ? launch_many<true>(a, s) : launch_many<false>(a, s);
   if (rc != INV_OK) return rc;
-  return launch_fold(a, s);
+  return last ? INV_OK : launch_fold(a, s);
 }
 
 }  // extern "C"
