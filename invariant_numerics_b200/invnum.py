@@ -353,48 +353,68 @@ def rmsnorm_bi(x, gamma, eps, want_y=True, want_split=False, stream=None):
 
 
 # ------------------------------------------- paged cache, draft verification --
+# These calls are short on the GPU: their checks are few Python steps, and
+# pointers go to the C call as plain integers.
 
-def _same_device(x, *others):
-    """The device of x, which must be the current one and hold the others too
-    (the C call launches on the current device's stream)."""
-    d = x.device
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.device != d:
-            raise ValueError(f"tensors are on different devices ({d}, {t.device})")
-    return d
+def _expect(t, dtype, dev, name, contiguous=True) -> None:
+    if t.dtype is not dtype or t.device != dev or not (t.is_contiguous() or not contiguous):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the others are on {dev}")
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _new(shape, dtype, device, stream):
+def _home(t):
+    """The device of a call's tensors, which must be the current one: the C
+    call launches there, on the current stream unless another is given."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _stream_id(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, dev, stream):
     """An uninitialised tensor of the stream the call runs on: memory that is
     freed after the call is reused behind it on that stream only."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _rows_of(t, name, width=None):
-    """fp32 [rows, width] with contiguous rows: its row stride."""
-    _need(t, torch.float32, name, contiguous=False)
-    if t.dim() != 2 or (width is not None and t.shape[1] != width) or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, {width if width is not None else 'n'}] with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 class PagedKVCache:
     """INT16 KV cache in pages: codes [n_pages, n_kv_heads, page_size, 128], scales fp32 [n_pages, n_kv_heads,
-    page_size].  Wraps four tensors; `empty` allocates a zeroed pool."""
+    page_size].  Wraps four tensors for good; `empty` allocates a zeroed pool."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "n_kv_heads", "page_size", "device", "_struct", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale):
-        _need(k, torch.int16, "k"), _need(v, torch.int16, "v")
-        _need(k_scale, torch.float32, "k_scale"), _need(v_scale, torch.float32, "v_scale")
-        if k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+        dev = k.device
+        _expect(k, torch.int16, dev, "k"), _expect(v, torch.int16, dev, "v")
+        _expect(k_scale, torch.float32, dev, "k_scale"), _expect(v_scale, torch.float32, dev, "v_scale")
+        shape = k.shape
+        if len(shape) != 4 or v.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
             raise ValueError("a paged cache is codes [n_pages, n_kv_heads, page_size, 128] and scales of its first "
                              "three dims, for k and v")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        if dev.type != "cuda":
+            raise ValueError("k must be a CUDA tensor")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, dev
+        self.n_pages, self.n_kv_heads, self.page_size, head_dim = shape
+        self._struct = PagedKVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape)
+        self._ref = C.byref(self._struct)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, device="cuda"):
@@ -403,19 +423,19 @@ class PagedKVCache:
         return cls(codes(), codes(), scale(), scale())
 
     def struct(self) -> PagedKVCacheStruct:
-        return PagedKVCacheStruct(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                                  self.v_scale.data_ptr(), self.n_pages, self.n_kv_heads, self.page_size,
-                                  self.head_dim)
+        return self._struct
 
 
-def _ragged(cache, page_table, q_start, lens):
+def _ragged(cache, page_table, q_start, lens, dev) -> int:
     """Checks the descriptors of a ragged batch; the number of sequences."""
-    for t, name in ((page_table, "page_table"), (q_start, "q_start"), (lens, "lens")):
-        _need(t, torch.int32, name)
-    n = lens.shape[0]
-    if page_table.dim() != 2 or page_table.shape[0] != n or lens.dim() != 1 or q_start.shape != (n + 1,):
+    _expect(page_table, torch.int32, dev, "page_table"), _expect(q_start, torch.int32, dev, "q_start")
+    _expect(lens, torch.int32, dev, "lens")
+    n = lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n or lens.dim() != 1 or q_start.dim() != 1 or \
+            q_start.numel() != n + 1:
         raise ValueError("page_table [n, pages], q_start [n + 1] and lens [n] must agree on the number of sequences")
-    _same_device(lens, page_table, q_start, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    if cache.device != dev:
+        raise ValueError(f"the cache is on {cache.device}, the others are on {dev}")
     return n
 
 
@@ -424,27 +444,35 @@ def kv_append_paged(qkv, cache: PagedKVCache, page_table, q_start, lens, rope_co
     """fp32 qkv [T, (Hq + 2 Hkv) * 128] of the new tokens of a ragged batch -> q fp32 [T, Hq, 128] (normed where
     q_gain is given, rotated); K (normed where k_gain is given, rotated) and V go to the cache.  Without q_out, the
     rows of no sequence are unspecified."""
-    n = _ragged(cache, page_table, q_start, lens)
-    ld = _rows_of(qkv, "qkv")
-    _need(rope_cos, torch.float32, "rope_cos"), _need(rope_sin, torch.float32, "rope_sin")
-    T, Hq = qkv.shape[0], qkv.shape[1] // HEAD_DIM - 2 * cache.n_kv_heads
-    if Hq <= 0 or qkv.shape[1] % HEAD_DIM:
+    dev = _home(qkv)
+    n = _ragged(cache, page_table, q_start, lens, dev)
+    _expect(qkv, torch.float32, dev, "qkv", contiguous=False)
+    _expect(rope_cos, torch.float32, dev, "rope_cos"), _expect(rope_sin, torch.float32, dev, "rope_sin")
+    if qkv.dim() != 2 or qkv.stride(1) != 1:
+        raise ValueError("qkv must be [T, heads * 128] with contiguous rows")
+    T, width = qkv.shape
+    Hq = width // HEAD_DIM - 2 * cache.n_kv_heads
+    if Hq <= 0 or width % HEAD_DIM:
         raise ValueError("qkv must hold n_heads + 2 * n_kv_heads heads of 128")
     if rope_cos.dim() != 2 or rope_cos.shape[1] != HEAD_DIM // 2 or rope_sin.shape != rope_cos.shape:
         raise ValueError("rope_cos and rope_sin must be [max_pos, 64]")
     for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-        if g is not None and _need(g, torch.float32, name).shape != (HEAD_DIM,):
-            raise ValueError(f"{name} must be [128]")
-    _same_device(lens, qkv, rope_cos, rope_sin, q_gain, k_gain, q_out)
+        if g is not None:
+            _expect(g, torch.float32, dev, name)
+            if g.numel() != HEAD_DIM:
+                raise ValueError(f"{name} must be [128]")
     if q_out is None:
-        q_out = _new((T, Hq, HEAD_DIM), torch.float32, qkv.device, stream)
-    elif _need(q_out, torch.float32, "q_out").shape != (T, Hq, HEAD_DIM):
-        raise ValueError(f"q_out must be [{T}, {Hq}, 128]")
-    cs = cache.struct()
-    _check("kv_append_paged",
-           lib.kv_append_paged(_ptr(qkv), ld, T, Hq, C.byref(cs), _ptr(page_table), page_table.shape[1], n,
-                               _ptr(q_start), _ptr(lens), _ptr(rope_cos), _ptr(rope_sin), rope_cos.shape[0],
-                               _ptr(q_gain), _ptr(k_gain), float(eps), _ptr(q_out), _stream(stream)))
+        q_out = _new((T, Hq, HEAD_DIM), torch.float32, dev, stream)
+    else:
+        _expect(q_out, torch.float32, dev, "q_out")
+        if q_out.shape != (T, Hq, HEAD_DIM):
+            raise ValueError(f"q_out must be [{T}, {Hq}, 128]")
+    rc = lib.kv_append_paged(qkv.data_ptr(), qkv.stride(0) if T > 1 else width, T, Hq, cache._ref,
+                             page_table.data_ptr(), page_table.shape[1], n, q_start.data_ptr(), lens.data_ptr(),
+                             rope_cos.data_ptr(), rope_sin.data_ptr(), rope_cos.shape[0], _addr(q_gain), _addr(k_gain),
+                             eps, q_out.data_ptr(), _stream_id(stream, dev))
+    if rc:
+        raise InvError("kv_append_paged", rc)
     return q_out
 
 
@@ -457,42 +485,58 @@ def attn_paged(q, cache: PagedKVCache, page_table, q_start, lens, softmax_scale,
                out=None, want_split=False, workspace=None, stream=None):
     """Causal attention of a ragged batch's new tokens over their pages: q fp32 [T, Hq, 128] -> out fp32 [T, Hq, 128]
     (and hi/lo if want_split).  Without out, the rows of no sequence are unspecified."""
-    n = _ragged(cache, page_table, q_start, lens)
-    _need(q, torch.float32, "q", contiguous=False)
+    dev = _home(q)
+    n = _ragged(cache, page_table, q_start, lens, dev)
+    _expect(q, torch.float32, dev, "q", contiguous=False)
     if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != HEAD_DIM):
         raise ValueError("q must be [T, n_heads, 128] with contiguous rows")
     T, Hq, _ = q.shape
-    ld = q.stride(0) if T > 1 else Hq * HEAD_DIM
-    room = page_table.shape[1] * cache.page_size
-    mq = T if max_q_bound is None or max_q_bound <= 0 else min(int(max_q_bound), T)
-    mlb = room if max_len_bound is None or max_len_bound <= 0 else min(int(max_len_bound), room)
-    _same_device(lens, q, out, workspace)
+    pages = page_table.shape[1]
+    room = pages * cache.page_size
+    mq = T if max_q_bound is None or not 0 < max_q_bound < T else int(max_q_bound)
+    mlb = room if max_len_bound is None or not 0 < max_len_bound < room else int(max_len_bound)
     if out is None:
-        out = _new((T, Hq, HEAD_DIM), torch.float32, q.device, stream)
-    elif _need(out, torch.float32, "out").shape != q.shape:
-        raise ValueError("out must have q's shape")
-    hi, lo = (_new(q.shape, torch.float16, q.device, stream) if want_split else None for _ in range(2))
+        out = _new((T, Hq, HEAD_DIM), torch.float32, dev, stream)
+    else:
+        _expect(out, torch.float32, dev, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    hi = lo = None
+    if want_split:
+        hi, lo = _new(q.shape, torch.float16, dev, stream), _new(q.shape, torch.float16, dev, stream)
     if workspace is None:
         nbytes = lib.attn_paged_workspace_size(T, n, Hq, cache.n_kv_heads, mq, mlb)
-        workspace = _new((max(nbytes, 16),), torch.uint8, q.device, stream)
-    cs = cache.struct()
-    _check("attn_paged",
-           lib.attn_paged(_ptr(q), ld, T, Hq, C.byref(cs), _ptr(page_table), page_table.shape[1], n, _ptr(q_start),
-                          _ptr(lens), mq, mlb, float(softmax_scale), _ptr(out), _ptr(hi), _ptr(lo), _ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _stream(stream)))
+        if nbytes:
+            workspace = _new((nbytes,), torch.uint8, dev, stream)
+    else:
+        _expect(workspace, workspace.dtype, dev, "workspace")
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = lib.attn_paged(q.data_ptr(), q.stride(0) if T > 1 else Hq * HEAD_DIM, T, Hq, cache._ref,
+                        page_table.data_ptr(), pages, n, q_start.data_ptr(), lens.data_ptr(), mq, mlb, softmax_scale,
+                        out.data_ptr(), _addr(hi), _addr(lo), _addr(workspace), nbytes, _stream_id(stream, dev))
+    if rc:
+        raise InvError("attn_paged", rc)
     return (out, hi, lo) if want_split else out
 
 
 def softmax_rows(logits, inv_temperature=1.0, out=None, stream=None):
     """fp32 logits [rows, n] -> probabilities of logits * inv_temperature (out may be logits)."""
-    ld = _rows_of(logits, "logits")
-    _same_device(logits, out)
+    dev = _home(logits)
+    _expect(logits, torch.float32, dev, "logits", contiguous=False)
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [rows, n] with contiguous rows")
+    rows, n = logits.shape
     if out is None:
-        out = _new(logits.shape, torch.float32, logits.device, stream)
-    elif out.shape != logits.shape:
-        raise ValueError("out must have the shape of logits")
-    _check("softmax_rows", lib.softmax_rows(_ptr(logits), logits.shape[0], logits.shape[1], ld, float(inv_temperature),
-                                            _ptr(out), _rows_of(out, "out"), _stream(stream)))
+        out = _new((rows, n), torch.float32, dev, stream)
+    else:
+        _expect(out, torch.float32, dev, "out", contiguous=False)
+        if out.shape != logits.shape or out.stride(1) != 1:
+            raise ValueError("out must have the shape of logits and contiguous rows")
+    many = rows > 1
+    rc = lib.softmax_rows(logits.data_ptr(), rows, n, logits.stride(0) if many else n, inv_temperature, out.data_ptr(),
+                          out.stride(0) if many else n, _stream_id(stream, dev))
+    if rc:
+        raise InvError("softmax_rows", rc)
     return out
 
 
@@ -501,28 +545,38 @@ def spec_verify(target, draft, draft_tokens, u_accept, u_sample, n_draft=None, t
     """Verifies drafted tokens int32 [B, m] against target probabilities fp32 [B, m + 1, V] and draft probabilities
     fp32 [B, m, V] (or None) with the uniforms u_accept [B, m] and u_sample [B]: tokens int32 [B, m + 1] (accepted,
     next, then -1) and n_accepted int32 [B]."""
-    _need(target, torch.float32, "target"), _need(draft_tokens, torch.int32, "draft_tokens")
-    _need(u_accept, torch.float32, "u_accept"), _need(u_sample, torch.float32, "u_sample")
+    dev = _home(target)
+    _expect(target, torch.float32, dev, "target"), _expect(draft_tokens, torch.int32, dev, "draft_tokens")
+    _expect(u_accept, torch.float32, dev, "u_accept"), _expect(u_sample, torch.float32, dev, "u_sample")
     B, m1, V = target.shape
     m = m1 - 1
     if draft_tokens.shape != (B, m) or u_accept.shape != (B, m) or u_sample.shape != (B,):
         raise ValueError("target [B, m + 1, V], draft_tokens and u_accept [B, m] and u_sample [B] must agree")
-    if draft is not None and _need(draft, torch.float32, "draft").shape != (B, m, V):
-        raise ValueError("draft must be [B, m, V]")
-    if n_draft is not None and _need(n_draft, torch.int32, "n_draft").shape != (B,):
-        raise ValueError("n_draft must be [B]")
-    _same_device(target, draft, draft_tokens, u_accept, u_sample, n_draft, tokens, n_accepted)
+    if draft is not None:
+        _expect(draft, torch.float32, dev, "draft")
+        if draft.shape != (B, m, V):
+            raise ValueError("draft must be [B, m, V]")
+    if n_draft is not None:
+        _expect(n_draft, torch.int32, dev, "n_draft")
+        if n_draft.shape != (B,):
+            raise ValueError("n_draft must be [B]")
     if tokens is None:
-        tokens = _new((B, m1), torch.int32, target.device, stream)
-    elif _need(tokens, torch.int32, "tokens").shape != (B, m1):
-        raise ValueError("tokens must be [B, m + 1]")
+        tokens = _new((B, m1), torch.int32, dev, stream)
+    else:
+        _expect(tokens, torch.int32, dev, "tokens")
+        if tokens.shape != (B, m1):
+            raise ValueError("tokens must be [B, m + 1]")
     if n_accepted is None:
-        n_accepted = _new((B,), torch.int32, target.device, stream)
-    elif _need(n_accepted, torch.int32, "n_accepted").shape != (B,):
-        raise ValueError("n_accepted must be [B]")
-    _check("spec_verify", lib.spec_verify(_ptr(target), V, _ptr(draft), V, B, m, V, _ptr(draft_tokens), _ptr(n_draft),
-                                          _ptr(u_accept), _ptr(u_sample), _ptr(tokens), _ptr(n_accepted),
-                                          _stream(stream)))
+        n_accepted = _new((B,), torch.int32, dev, stream)
+    else:
+        _expect(n_accepted, torch.int32, dev, "n_accepted")
+        if n_accepted.shape != (B,):
+            raise ValueError("n_accepted must be [B]")
+    rc = lib.spec_verify(target.data_ptr(), V, _addr(draft), V, B, m, V, draft_tokens.data_ptr(), _addr(n_draft),
+                         u_accept.data_ptr(), u_sample.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(),
+                         _stream_id(stream, dev))
+    if rc:
+        raise InvError("spec_verify", rc)
     return tokens, n_accepted
 
 

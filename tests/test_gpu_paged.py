@@ -584,6 +584,35 @@ def test_speculative_step_equals_one_token_at_a_time(inv):
     assert status() == inv.INV_OK
 
 
+def test_binding_refuses_wrong_tensors(inv):
+    """Types, shapes and strides the operators do not take."""
+    n_pages, table, start, ln = batch([20], [2], 16, seed=1)
+    cache = pool(inv, n_pages, 2, 16, seed=2)
+    q = torch.zeros(2, 4, 128, device="cuda")
+    ok = lambda **kw: inv.attn_paged(**{**dict(q=q, cache=cache, page_table=table, q_start=start, lens=ln,
+                                               softmax_scale=SCALE), **kw})
+    ok()
+    for bad in (dict(q=q.half()), dict(q=q[:, :, :64]), dict(q=q.transpose(0, 1)), dict(page_table=table.long()),
+                dict(page_table=table[0]), dict(q_start=start[:1]), dict(lens=ln.float()), dict(out=q[:1]),
+                dict(lens=ln.cpu())):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(inv.InvError):
+        ok(q=torch.zeros(2, 3, 128, device="cuda"))  # 3 heads over 2 kv heads
+    with pytest.raises(inv.InvError):
+        ok(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), max_len_bound=0, page_table=table.repeat(1, 40))
+    with pytest.raises(ValueError):
+        inv.PagedKVCache(cache.k.float(), cache.v, cache.k_scale, cache.v_scale)
+    with pytest.raises(ValueError):
+        inv.kv_append_paged(torch.zeros(2, 500, device="cuda"), cache, table, start, ln, *tables(inv, 64))
+    with pytest.raises(ValueError):
+        inv.softmax_rows(torch.zeros(4, 6, device="cuda").t())
+    with pytest.raises(ValueError):
+        inv.spec_verify(torch.zeros(1, 3, 5, device="cuda"), None, i32([[1]]), torch.zeros(1, 1, device="cuda"),
+                        torch.zeros(1, device="cuda"))
+    assert status() == inv.INV_OK
+
+
 def test_the_index_checking_build_agrees(inv):
     """These tests on the build that checks every index: nothing leaves its buffer."""
     import os

@@ -106,3 +106,16 @@ def test_verify_refusals(inv):
     assert call(a1=99) == INVALID and call(a3=99) == INVALID
     for i in (0, 7, 9, 10, 11, 12):
         assert call(**{f"a{i}": None}) == INVALID, i
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes(inv):
+    import torch
+    z = torch.zeros
+    with pytest.raises(ValueError, match="CUDA"):
+        inv.PagedKVCache(z(2, 1, 16, 128, dtype=torch.int16), z(2, 1, 16, 128, dtype=torch.int16), z(2, 1, 16), z(2, 1, 16))
+    with pytest.raises(ValueError, match="paged cache"):
+        inv.PagedKVCache(z(2, 1, 16, 128, dtype=torch.int16), z(2, 1, 16, 64, dtype=torch.int16), z(2, 1, 16), z(2, 1, 16))
+    with pytest.raises(ValueError, match="CUDA"):
+        inv.softmax_rows(z(2, 5))
+    with pytest.raises(ValueError, match="CUDA"):
+        inv.spec_verify(z(1, 2, 5), None, z(1, 1, dtype=torch.int32), z(1, 1), z(1))
