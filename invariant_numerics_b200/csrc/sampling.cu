@@ -1,87 +1,174 @@
 // softmax_rows and spec_verify: from logits to the tokens of a verification
 // step of speculative decoding.
 #include "common.cuh"
-#include "paged.cuh"
 
 namespace {
 
 using inv::record_status;
 
-// ----------------------------------------------------------- softmax_rows ----
-
-constexpr int kSoftThreads = 1024;
-
-__device__ __forceinline__ float4 load4(const float* p, int i, int n) {
-  float4 v;
-  v.x = i < n ? p[i] : -INFINITY;
-  v.y = i + 1 < n ? p[i + 1] : -INFINITY;
-  v.z = i + 2 < n ? p[i + 2] : -INFINITY;
-  v.w = i + 3 < n ? p[i + 3] : -INFINITY;
-  return v;
+// ------------------------------------------------------------- clusters ----
+//
+// A row is split over the CTAs of a cluster, each keeping its part in registers,
+// so that the row is read once; the parts' results cross by stores into the
+// other CTAs' shared memory and one cluster barrier.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores 8 bytes at this CTA's shared address p, in the CTA of rank r.
+__device__ __forceinline__ void store_cluster(void* p, uint32_t r, uint64_t v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(inv::smem_u32(p)), "r"(r));
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
 }
 
-// One CTA per row; thread t owns the elements 4t .. 4t+3 of every 4096.
-__global__ void __launch_bounds__(kSoftThreads)
-    softmax_kernel(const float* __restrict__ x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y,
-                   int* status) {
-  __shared__ float red[32];
-  __shared__ float bc[2];
+constexpr int kMaxCluster = 8;
+
+// Elements i .. i+3 of a row of n; kVec: 16-byte aligned.
+template <bool kVec>
+__device__ __forceinline__ float4 load4(const float* p, int i, int n, float none) {
+  if (kVec && i + 3 < n) return *reinterpret_cast<const float4*>(p + i);
+  float4 v;
+  v.x = i < n ? p[i] : none;
+  v.y = i + 1 < n ? p[i + 1] : none;
+  v.z = i + 2 < n ? p[i + 2] : none;
+  v.w = i + 3 < n ? p[i + 3] : none;
+  return v;
+}
+template <bool kVec>
+__device__ __forceinline__ void store4(float* p, int i, int n, float4 v) {
+  if (kVec && i + 3 < n) {
+    *reinterpret_cast<float4*>(p + i) = v;
+    return;
+  }
+  if (i < n) p[i] = v.x;
+  if (i + 1 < n) p[i + 1] = v.y;
+  if (i + 2 < n) p[i + 2] = v.z;
+  if (i + 3 < n) p[i + 3] = v.w;
+}
+
+// ----------------------------------------------------------- softmax_rows ----
+//
+// HBM bound: 8 bytes an element.  Part c of a row (32 THR elements; thread t owns
+// the elements 4t .. 4t+3 of every 4 THR): m_c, s_c = sum exp((x - m_c) t); the row:
+// M = max m_c, S = sum_c s_c exp((m_c - M) t) in ascending c; y = exp((x - m_c) t)
+// (exp((m_c - M) t) / S).  THR and the number of parts follow from n alone, so the
+// order of the sum does too.
+constexpr int kSoftVec = 8;  // float4 a thread
+
+template <int THR>
+__device__ __forceinline__ float block_max(float m, float* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = red[lane & (THR / 32 - 1)];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+template <int THR>
+__device__ __forceinline__ float block_sum(float s, float* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+  if (lane == 0) red[warp] = s;
+  __syncthreads();
+  s = lane < THR / 32 ? red[lane] : 0.0f;
+#pragma unroll
+  for (int o = THR / 64; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+  return s;  // valid in lane 0 of every warp
+}
+
+template <int THR, bool kVec>
+__global__ void __launch_bounds__(THR)
+    softmax_kernel(const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, int* status) {
+  __shared__ float red_m[32], red_s[32];
+  __shared__ uint64_t parts[kMaxCluster];  // (m_c, s_c)
+  const uint32_t rank = cluster_rank(), parts_n = cluster_size();
+  cluster_arrive();  // (every CTA of the cluster runs before another stores into it)
+  const int64_t r = blockIdx.x / parts_n;
+  const int first = (int)rank * (THR * 4 * kSoftVec);
+  const bool in = INV_SPAN_IN_BOUNDS(status, r * ld, r * ld + n - 1, (int64_t)(rows - 1) * ld + n) &&
+                  INV_SPAN_IN_BOUNDS(status, r * ld_y, r * ld_y + n - 1, (int64_t)(rows - 1) * ld_y + n);
+  const int n_in = in ? n : 0;
+  const float* xr = x + r * ld;
+  float* yr = y + r * ld_y;
+  float4 v[kSoftVec];
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kSoftVec; ++j) v[j] = load4<kVec>(xr, first + 4 * (int)threadIdx.x + j * 4 * THR, n_in, -INFINITY);
+#pragma unroll
+  for (int j = 0; j < kSoftVec; ++j) m = fmaxf(m, fmaxf(fmaxf(v[j].x, v[j].y), fmaxf(v[j].z, v[j].w)));
+  m = block_max<THR>(m, red_m);
+  const bool none = m == -INFINITY;  // nothing but -inf in this part
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kSoftVec; ++j) {
+    v[j].x = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].x, m), it));
+    v[j].y = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].y, m), it));
+    v[j].z = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].z, m), it));
+    v[j].w = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].w, m), it));
+    s = __fadd_rn(s, __fadd_rn(__fadd_rn(v[j].x, v[j].y), __fadd_rn(v[j].z, v[j].w)));
+  }
+  s = block_sum<THR>(s, red_s);
+  cluster_wait();
+  if (threadIdx.x == 0) {
+    const uint64_t mine = ((uint64_t)__float_as_uint(s) << 32) | __float_as_uint(m);
+    for (uint32_t q = 0; q < parts_n; ++q) store_cluster(&parts[rank], q, mine);
+  }
+  cluster_arrive();
+  cluster_wait();
+  float M = -INFINITY, S = 0.0f;
+  for (uint32_t q = 0; q < parts_n; ++q) M = fmaxf(M, __uint_as_float((uint32_t)parts[q]));
+  for (uint32_t q = 0; q < parts_n; ++q) {
+    const float mq = __uint_as_float((uint32_t)parts[q]), sq = __uint_as_float((uint32_t)(parts[q] >> 32));
+    if (mq != -INFINITY) S = __fadd_rn(S, __fmul_rn(sq, expf(__fmul_rn(__fsub_rn(mq, M), it))));
+  }
+  const float f = none ? 0.0f : __fmul_rn(expf(__fmul_rn(__fsub_rn(m, M), it)), __frcp_rn(S));
+#pragma unroll
+  for (int j = 0; j < kSoftVec; ++j)
+    store4<kVec>(yr, first + 4 * (int)threadIdx.x + j * 4 * THR, n_in,
+                 make_float4(__fmul_rn(v[j].x, f), __fmul_rn(v[j].y, f), __fmul_rn(v[j].z, f), __fmul_rn(v[j].w, f)));
+}
+
+// Rows longer than eight parts: one CTA a row, which reads it three times.
+constexpr int kLongThreads = 1024;
+__global__ void __launch_bounds__(kLongThreads)
+    softmax_long_kernel(const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, int* status) {
+  __shared__ float red_m[32], red_s[32];
+  __shared__ float total;
   const int64_t r = blockIdx.x;
   if (!INV_SPAN_IN_BOUNDS(status, r * ld, r * ld + n - 1, (int64_t)(rows - 1) * ld + n) ||
       !INV_SPAN_IN_BOUNDS(status, r * ld_y, r * ld_y + n - 1, (int64_t)(rows - 1) * ld_y + n))
     return;
   const float* xr = x + r * ld;
   float* yr = y + r * ld_y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float m = -INFINITY;
-  for (int i = threadIdx.x * 4; i < n; i += 4 * kSoftThreads) {
-    const float4 v = load4(xr, i, n);
-    m = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  if (warp == 0) {
-    m = red[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) bc[0] = m;
-  }
-  __syncthreads();
-  m = bc[0];
+  for (int i = threadIdx.x; i < n; i += kLongThreads) m = fmaxf(m, xr[i]);
+  m = block_max<kLongThreads>(m, red_m);
   const bool none = m == -INFINITY;
-  const auto e = [&](float v) { return none ? 0.0f : expf(__fmul_rn(__fsub_rn(v, m), it)); };
   float s = 0.0f;
-  for (int i = threadIdx.x * 4; i < n; i += 4 * kSoftThreads) {
-    const float4 v = load4(xr, i, n);
-    s = __fadd_rn(s, __fadd_rn(__fadd_rn(e(v.x), e(v.y)), __fadd_rn(e(v.z), e(v.w))));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-  if (lane == 0) red[warp] = s;
+  for (int i = threadIdx.x; i < n; i += kLongThreads)
+    s = __fadd_rn(s, none ? 0.0f : expf(__fmul_rn(__fsub_rn(xr[i], m), it)));
+  s = block_sum<kLongThreads>(s, red_s);
+  if (threadIdx.x == 0) total = s;
   __syncthreads();
-  if (warp == 0) {
-    s = red[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-    if (lane == 0) bc[1] = s;
-  }
-  __syncthreads();
-  const float inv_s = none ? 0.0f : __frcp_rn(bc[1]);
-  for (int i = threadIdx.x * 4; i < n; i += 4 * kSoftThreads) {
-    const float4 v = load4(xr, i, n);
-    yr[i] = __fmul_rn(e(v.x), inv_s);
-    if (i + 1 < n) yr[i + 1] = __fmul_rn(e(v.y), inv_s);
-    if (i + 2 < n) yr[i + 2] = __fmul_rn(e(v.z), inv_s);
-    if (i + 3 < n) yr[i + 3] = __fmul_rn(e(v.w), inv_s);
-  }
+  const float f = none ? 0.0f : __frcp_rn(total);
+  for (int i = threadIdx.x; i < n; i += kLongThreads)
+    yr[i] = none ? 0.0f : __fmul_rn(expf(__fmul_rn(__fsub_rn(xr[i], m), it)), f);
 }
 
 // ------------------------------------------------------------ spec_verify ----
-
-constexpr int kVerifyThreads = 1024;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
 
 struct VerifyArgs {
   const float* target;
@@ -97,81 +184,240 @@ struct VerifyArgs {
   int32_t* n_accepted;
 };
 
-// One CTA per sequence.  Warp 0 decides the accepted prefix, 32 drafts a step.
-// The next token: warp w owns a contiguous range of the vocabulary; the warps'
-// totals in 64 bits tell which range the draw falls into, and that warp walks
-// its range again.
-__global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(VerifyArgs a, int* status) {
-  __shared__ int k_sh, m_sh;
-  __shared__ double tot[kVerifyWarps];
-  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The accepted prefix of sequence b, by one warp, 32 drafts a step: k, or -1 for
+// descriptors out of range; m = number of drafts.
+__device__ __forceinline__ int accepted_prefix(const VerifyArgs& a, int b, int lane, int& m, int* status, bool record) {
   const int D = a.max_draft, V = a.vocab;
   const int32_t* x = a.draft_tokens + (int64_t)b * D;
-  if (warp == 0) {
-    const int m = a.n_draft ? a.n_draft[b] : D;
-    bool bad = m < 0 || m > D;
-    int k = 0;
-    if (!bad) {
-      k = m;
-      for (int i0 = 0; i0 < m; i0 += 32) {
-        const int i = i0 + lane;
-        bool ok = true, wrong = false;
-        if (i < m) {
-          const int t = x[i];
-          wrong = t < 0 || t >= V;
-          if (!wrong) {
-            const double q = a.draft ? (double)a.draft[((int64_t)b * D + i) * a.ld_d + t] : 1.0;
-            ok = (double)a.u_accept[(int64_t)b * D + i] * q < (double)a.target[((int64_t)b * (D + 1) + i) * a.ld_t + t];
-          }
-        }
-        bad |= __any_sync(0xffffffffu, wrong);
-        const unsigned no = __ballot_sync(0xffffffffu, !ok);
-        if (no != 0 && k == m) k = i0 + __ffs(no) - 1;
+  m = a.n_draft ? a.n_draft[b] : D;
+  bool bad = m < 0 || m > D;
+  int k = bad ? -1 : m;
+  for (int i0 = 0; !bad && i0 < m; i0 += 32) {
+    const int i = i0 + lane;
+    bool ok = true, wrong = false;
+    if (i < m) {
+      const int t = x[i];
+      wrong = t < 0 || t >= V;
+      if (!wrong) {
+        const double q = a.draft ? (double)a.draft[((int64_t)b * D + i) * a.ld_d + t] : 1.0;
+        ok = (double)a.u_accept[(int64_t)b * D + i] * q < (double)a.target[((int64_t)b * (D + 1) + i) * a.ld_t + t];
       }
     }
+    bad = __any_sync(0xffffffffu, wrong);
+    const unsigned no = __ballot_sync(0xffffffffu, !ok);
+    if (no != 0 && k == m) k = i0 + __ffs(no) - 1;
+  }
+  if (bad && record && lane == 0) record_status(status, INV_ERR_INVALID_ARG);
+  return bad ? -1 : k;
+}
+
+// Everything of the outputs but the next token.
+__device__ __forceinline__ void write_prefix(const VerifyArgs& a, int b, int k) {
+  const int D = a.max_draft;
+  const int32_t* x = a.draft_tokens + (int64_t)b * D;
+  int32_t* out = a.tokens + (int64_t)b * (D + 1);
+  for (int i = threadIdx.x; i <= D; i += blockDim.x)
+    if (i != k) out[i] = i < k ? x[i] : -1;
+  if (threadIdx.x == 0) a.n_accepted[b] = k < 0 ? 0 : k;
+}
+
+__device__ __forceinline__ double weight(float p, float q) { return p > q ? (double)p - (double)q : 0.0; }
+
+// One cluster per sequence; CTA c owns 16 THR entries of the row, warp w of it a
+// run of 512, lane l the entries 4l .. 4l+3 of every 128: 16 in registers.  The
+// first dependent reads decide k, then the rows p_k and q_k are read once.  Sums in
+// 64 bits: lane, warp, CTA, cluster totals tell which CTA, then which warp and which
+// 128 entries the draw falls into; a scan of their lanes ends the search.
+// Latency bound (four dependent reads); 8 bytes a vocabulary entry are read.
+template <int THR, bool kVec>
+__global__ void __launch_bounds__(THR) spec_verify_kernel(const VerifyArgs a, int* status) {
+  constexpr int W = THR / 32;
+  __shared__ int km[2];
+  __shared__ double warp_tot[W];
+  __shared__ uint64_t part_tot[2][kMaxCluster];
+  const uint32_t rank = cluster_rank(), parts = cluster_size();
+  cluster_arrive();
+  const int b = (int)(blockIdx.x / parts), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = a.max_draft, V = a.vocab;
+  if (warp == 0) {
+    int m;
+    const int k = accepted_prefix(a, b, lane, m, status, rank == 0);
     if (lane == 0) {
-      if (bad) record_status(status, INV_ERR_INVALID_ARG);
-      k_sh = bad ? -1 : k;
-      m_sh = m;
+      km[0] = k;
+      km[1] = m;
     }
   }
   __syncthreads();
-  const int k = k_sh, m = m_sh;
+  const int k = km[0], m = km[1];
+  if (rank == 0) write_prefix(a, b, k);
   int32_t* out = a.tokens + (int64_t)b * (D + 1);
-  if (k < 0) {
-    for (int i = threadIdx.x; i <= D; i += kVerifyThreads) out[i] = -1;
-    if (threadIdx.x == 0) a.n_accepted[b] = 0;
-    return;
-  }
-  for (int i = threadIdx.x; i <= D; i += kVerifyThreads)
-    if (i != k) out[i] = i < k ? x[i] : -1;
-  if (threadIdx.x == 0) a.n_accepted[b] = k;
-
+  cluster_wait();
+  if (k < 0) return;  // (the same in the whole cluster)
   const float* p = a.target + ((int64_t)b * (D + 1) + k) * a.ld_t;
   const float* q = k < m && a.draft ? a.draft + ((int64_t)b * D + k) * a.ld_d : nullptr;
-  const int drop = k < m && !a.draft ? x[k] : -1;
+  const int drop = k < m && !a.draft ? a.draft_tokens[(int64_t)b * D + k] : -1;
+  const int e0 = ((int)rank * W + warp) * 512 + 4 * lane;
+  float4 pv[4], qv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pv[i] = load4<kVec>(p, e0 + 128 * i, V, 0.0f);
+    qv[i] = q ? load4<kVec>(q, e0 + 128 * i, V, 0.0f) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (drop >= 0) {  // a looked-up draft has q = 1 there (probabilities are at most 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + 128 * i;
+      if (drop == e) pv[i].x = 0.0f;
+      if (drop == e + 1) pv[i].y = 0.0f;
+      if (drop == e + 2) pv[i].z = 0.0f;
+      if (drop == e + 3) pv[i].w = 0.0f;
+    }
+  }
+  const double u = a.u_sample[b];
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {  // second round: the fallback to the target's own weights
+    double d[4];  // this lane's four entries of each 128
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d[i] = (weight(pv[i].x, qv[i].x) + weight(pv[i].y, qv[i].y)) + (weight(pv[i].z, qv[i].z) + weight(pv[i].w, qv[i].w));
+      s += d[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) warp_tot[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+      double t = 0.0;
+      for (int w = 0; w < W; ++w) t += warp_tot[w];
+      if (lane < parts) store_cluster(&part_tot[round][rank], lane, (uint64_t)__double_as_longlong(t));
+    }
+    cluster_arrive();
+    cluster_wait();
+    double total = 0.0;
+    for (uint32_t c = 0; c < parts; ++c) total += __longlong_as_double((long long)part_tot[round][c]);
+    if (total > 0.0) {
+      const double thr = u * total;
+      // the first part whose end lies beyond the draw (else the last one with weight), then likewise its warp
+      uint32_t pick = 0;
+      double run = 0.0, before = 0.0;
+      for (uint32_t c = 0; c < parts; ++c) {
+        const double t = __longlong_as_double((long long)part_tot[round][c]);
+        if (t > 0.0) {
+          pick = c;
+          before = run;
+          if (run + t > thr) break;
+        }
+        run += t;
+      }
+      if (rank != pick) return;
+      int pw = 0;
+      run = before;
+      for (int w = 0; w < W; ++w) {
+        const double t = warp_tot[w];
+        if (t > 0.0) {
+          pw = w;
+          before = run;
+          if (run + t > thr) break;
+        }
+        run += t;
+      }
+      if (warp != pw) return;
+      int last = -1;
+      double c0 = before;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        // (registers are not indexed: the four are rotated)
+        const float4 x = pv[0], y = qv[0];
+        const double di = d[0];
+        pv[0] = pv[1], pv[1] = pv[2], pv[2] = pv[3];
+        qv[0] = qv[1], qv[1] = qv[2], qv[2] = qv[3];
+        d[0] = d[1], d[1] = d[2], d[2] = d[3];
+        double c = di;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double up = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += up;
+        }
+        const unsigned some = __ballot_sync(0xffffffffu, di > 0.0);
+        const unsigned hit = __ballot_sync(0xffffffffu, di > 0.0 && c0 + c > thr);
+        if (some) {
+          // the lane whose four entries hold the draw (else the last one with weight)
+          const int l = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+          const double w[4] = {weight(x.x, y.x), weight(x.y, y.y), weight(x.z, y.z), weight(x.w, y.w)};
+          double cc = c0 + (c - di);
+          int j = -1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool past = j >= 0 && cc > thr;  // an earlier entry already exceeds the draw
+            cc += w[e];
+            if (w[e] > 0.0 && !past) j = e;
+          }
+          last = __shfl_sync(0xffffffffu, e0 + 128 * i + j, l);
+        }
+        if (hit) break;
+        c0 += __shfl_sync(0xffffffffu, c, 31);
+      }
+      if (lane == 0) out[k] = last;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pv[i] = load4<kVec>(p, e0 + 128 * i, V, 0.0f);
+      qv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+  }
+  if (rank == 0 && threadIdx.x == 0) out[k] = -1;
+}
+
+// Vocabularies longer than a cluster holds: one CTA a sequence, a contiguous range
+// a warp, and the warp the draw falls into walks its range again.
+constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+__global__ void __launch_bounds__(kVerifyThreads) spec_verify_long_kernel(const VerifyArgs a, int* status) {
+  __shared__ int km[2];
+  __shared__ double tot[kVerifyWarps];
+  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = a.max_draft, V = a.vocab;
+  if (warp == 0) {
+    int m;
+    const int k = accepted_prefix(a, b, lane, m, status, true);
+    if (lane == 0) {
+      km[0] = k;
+      km[1] = m;
+    }
+  }
+  __syncthreads();
+  const int k = km[0], m = km[1];
+  write_prefix(a, b, k);
+  if (k < 0) return;
+  int32_t* out = a.tokens + (int64_t)b * (D + 1);
+  const float* p = a.target + ((int64_t)b * (D + 1) + k) * a.ld_t;
+  const float* q = k < m && a.draft ? a.draft + ((int64_t)b * D + k) * a.ld_d : nullptr;
+  const int drop = k < m && !a.draft ? a.draft_tokens[(int64_t)b * D + k] : -1;
   const int range = ((V + kVerifyWarps - 1) / kVerifyWarps + 31) / 32 * 32;
   const int j0 = min(V, warp * range), j1 = min(V, j0 + range);
-  for (int plain = 0; plain < 2; ++plain) {  // second time: the fallback to the target's own weights
-    const auto weight = [&](int j) {
-      const double t = p[j];
-      if (plain) return t > 0.0 ? t : 0.0;
-      const double u = q ? (double)q[j] : 0.0;
-      return j != drop && t > u ? t - u : 0.0;
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    const auto at = [&](int j) {
+      if (round) return weight(p[j], 0.0f);
+      return j == drop ? 0.0 : weight(p[j], q ? q[j] : 0.0f);
     };
     double s = 0.0;
-    for (int j = j0 + lane; j < j1; j += 32) s += weight(j);
+    for (int j = j0 + lane; j < j1; j += 32) s += at(j);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) tot[warp] = s;
     __syncthreads();
-    double total = 0.0, before = 0.0;
+    double total = 0.0;
+#pragma unroll 1
     for (int w = 0; w < kVerifyWarps; ++w) total += tot[w];
     if (total > 0.0) {
       const double thr = (double)a.u_sample[b] * total;
-      // the first range whose end lies beyond the draw (else the last one with weight)
-      int pick = -1;
-      double run = 0.0;
+      int pick = 0;
+      double run = 0.0, before = 0.0;
+#pragma unroll 1
       for (int w = 0; w < kVerifyWarps; ++w) {
         if (tot[w] > 0.0) {
           pick = w;
@@ -180,33 +426,65 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(VerifyArgs 
         }
         run += tot[w];
       }
-      if (warp == pick) {
-        int last = -1;
-        double c0 = before;
-        for (int j = j0; j < j1; j += 32) {
-          const double w = j + lane < j1 ? weight(j + lane) : 0.0;
-          double c = w;
+      if (warp != pick) return;
+      int last = -1;
+      double c0 = before;
+      for (int j = j0; j < j1; j += 32) {
+        const double w = j + lane < j1 ? at(j + lane) : 0.0;
+        double c = w;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, c, o);
-            if (lane >= o) c += up;
-          }
-          const unsigned pos = __ballot_sync(0xffffffffu, w > 0.0);
-          const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && c0 + c > thr);
-          if (pos) last = j + 31 - __clz(pos);
-          if (hit) {
-            last = j + __ffs(hit) - 1;
-            break;
-          }
-          c0 += __shfl_sync(0xffffffffu, c, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const double up = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += up;
         }
-        if (lane == 0) out[k] = last;
+        const unsigned some = __ballot_sync(0xffffffffu, w > 0.0);
+        const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && c0 + c > thr);
+        if (some) last = j + 31 - __clz(some);
+        if (hit) {
+          last = j + __ffs(hit) - 1;
+          break;
+        }
+        c0 += __shfl_sync(0xffffffffu, c, 31);
       }
+      if (lane == 0) out[k] = last;
       return;
     }
     __syncthreads();
   }
   if (threadIdx.x == 0) out[k] = -1;
+}
+
+// Launches `kernel` with `rows` clusters of `parts` CTAs.
+template <class K, class... Args>
+int launch_clusters(K kernel, int64_t rows, int parts, int threads, cudaStream_t s, Args... args) {
+  if (rows * parts > 0x7fffffff) return INV_ERR_UNSUPPORTED_SHAPE;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(rows * parts));
+  lc.blockDim = dim3(threads);
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, kernel, args...) != cudaSuccess) return INV_ERR_CUDA;
+  INV_CHECK_LAUNCH();
+  return INV_OK;
+}
+
+template <int THR>
+int launch_softmax(bool vec, const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, cudaStream_t s) {
+  const int part = THR * 4 * kSoftVec, parts = (n + part - 1) / part;
+  return launch_clusters(vec ? softmax_kernel<THR, true> : softmax_kernel<THR, false>, rows, parts, THR, s, x, rows, n, ld,
+                         it, y, ld_y, inv::status_ptr());
+}
+
+template <int THR>
+int launch_verify(bool vec, const VerifyArgs& a, cudaStream_t s) {
+  const int part = THR * 16, parts = (a.vocab + part - 1) / part;
+  return launch_clusters(vec ? spec_verify_kernel<THR, true> : spec_verify_kernel<THR, false>, a.B, parts, THR, s, a,
+                         inv::status_ptr());
 }
 
 }  // namespace
@@ -219,8 +497,14 @@ int softmax_rows(const float* logits, int rows, int n, int64_t ld, float inv_tem
   if (!(inv_temperature > 0.0f) || !(inv_temperature <= 3.402823466e38f)) return INV_ERR_INVALID_ARG;
   if (rows == 0) return INV_OK;
   if (!logits || !probs || (logits == probs && ld != ld_p)) return INV_ERR_INVALID_ARG;
-  softmax_kernel<<<(unsigned)rows, kSoftThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      logits, rows, n, ld, inv_temperature, probs, ld_p, inv::status_ptr());
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool vec = inv::aligned16(logits) && inv::aligned16(probs) && ld % 4 == 0 && ld_p % 4 == 0;
+  // The smallest CTAs whose cluster of at most eight holds a row: many small CTAs overlap their loads, exponentials and
+  // stores (320 rows of 32000: 4 CTAs of 256 threads a row 17.6 us, 1 of 1024 24.9 us).
+  if (n <= kMaxCluster * 256 * 4 * kSoftVec) return launch_softmax<256>(vec, logits, rows, n, ld, inv_temperature, probs, ld_p, s);
+  if (n <= kMaxCluster * 1024 * 4 * kSoftVec) return launch_softmax<1024>(vec, logits, rows, n, ld, inv_temperature, probs, ld_p, s);
+  softmax_long_kernel<<<(unsigned)rows, kLongThreads, 0, s>>>(logits, rows, n, ld, inv_temperature, probs, ld_p,
+                                                              inv::status_ptr());
   INV_CHECK_LAUNCH();
   return INV_OK;
 }
@@ -235,7 +519,11 @@ int spec_verify(const float* target, int64_t ld_target, const float* draft, int6
     return INV_ERR_INVALID_ARG;
   const VerifyArgs a = {target,  ld_target,    draft,   ld_draft, B,        max_draft, vocab,
                         draft_tokens, n_draft, u_accept, u_sample, tokens, n_accepted};
-  spec_verify_kernel<<<(unsigned)B, kVerifyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, inv::status_ptr());
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool vec = inv::aligned16(target) && inv::aligned16(draft) && ld_target % 4 == 0 && ld_draft % 4 == 0;
+  if (vocab <= kMaxCluster * 256 * 16) return launch_verify<256>(vec, a, s);
+  if (vocab <= kMaxCluster * 1024 * 16) return launch_verify<1024>(vec, a, s);
+  spec_verify_long_kernel<<<(unsigned)B, kVerifyThreads, 0, s>>>(a, inv::status_ptr());
   INV_CHECK_LAUNCH();
   return INV_OK;
 }

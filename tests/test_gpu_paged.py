@@ -415,7 +415,8 @@ def test_kv_append_paged_bad_descriptors_are_recorded(inv):
 # ----------------------------------------------------- softmax, verification ---
 
 @pytest.mark.parametrize("rows,n,it", [(1, 1, 1.0), (3, 7, 0.5), (2, 1000, 1.0), (5, 4096, 2.0), (4, 4099, 1 / 0.7),
-                                       (2, 32003, 1.0), (3, 65537, 0.9), (2, 300001, 1.0)])
+                                       (2, 8192, 1.0), (2, 32003, 1.0), (3, 65536, 1.0),
+                                       (3, 65537, 0.9), (2, 262144, 1.0), (2, 300001, 1.0)])
 def test_softmax_rows_against_float64(inv, rows, n, it):
     x = torch.randn(rows, n, generator=gen(n), device="cuda") * 5
     x[:, ::13] = -math.inf
@@ -427,10 +428,11 @@ def test_softmax_rows_against_float64(inv, rows, n, it):
     it32 = float(np.float32(it))
     t = x.double() * it32
     want = torch.softmax(t, -1).nan_to_num(0.0)
-    # the exponent's rounding (two of 2^-24 of up to |t - max|), exp's 2 ulp, and the sum's and quotient's few
+    # in units of 2^-24: the exponent's two roundings (of up to |t - max|, in one or two pieces), exp's 2 ulp (4, twice
+    # where a row has parts), the factor's and the product's (3); the same of the sum's terms, and its additions
     span = (t.amax(-1, keepdim=True) - t).nan_to_num(0.0, posinf=0.0)
-    depth = n // 4096 + 20  # additions one term passes through
-    rel = 2.0 ** -24 * (2 * span + 4) + 2.0 ** -24 * (2 * (want * span).sum(-1, keepdim=True) + 4 + depth)
+    depth = n // 4096 + 32  # additions one term passes through
+    rel = 2.0 ** -24 * (2 * span + 11) + 2.0 ** -24 * (2 * (want * span).sum(-1, keepdim=True) + 9 + depth)
     assert ((y.double() - want).abs() <= rel * want + 1e-38).all()
     assert (y[:, ::13] == 0).all() if n > 1 else (y == 1).all()
     wide = torch.full((rows, n + 5), 1.0, device="cuda")
@@ -470,7 +472,9 @@ def verify64(target, draft, tokens, u, us, n_draft):
 
 
 @pytest.mark.parametrize("B,m,V,probs", [(1, 0, 5, True), (1, 1, 1, True), (3, 4, 1000, True), (2, 7, 32003, False),
-                                         (9, 40, 257, True), (4, 3, 131072, True), (64, 5, 4001, False)])
+                                         (9, 40, 257, True), (4, 3, 131072, True), (64, 5, 4001, False),
+                                         (2, 2, 4096, True), (3, 2, 32768, False), (3, 2, 32769, True), (2, 2, 131073, True),
+                                         (2, 1, 131075, False)])
 def test_spec_verify_against_float64(inv, B, m, V, probs):
     g = gen(B * 100 + m)
     logits = torch.randn(B, m + 1, V, generator=g, device="cuda") * 3
@@ -508,6 +512,17 @@ def test_spec_verify_edges(inv):
     # a lookup draft that is rejected is not drawn again
     t, a = inv.spec_verify(f([p + p]), None, i32([[0]]), f([[0.6]]), f([0.0]))
     assert a.tolist() == [0] and t.tolist() == [[1, -1]]
+    # the same in long rows, in every form of the kernel
+    for n in (5000, 40000, 140000):
+        row = torch.zeros(1, 2, n, device="cuda")
+        row[0, :, n - 7] = 0.75
+        row[0, :, 3] = 0.25
+        t, a = inv.spec_verify(row, row[:, :1].contiguous() * 2, i32([[3]]), f([[0.9]]), f([0.3]))
+        assert a.tolist() == [0] and t.tolist() == [[n - 7, -1]]
+        t, a = inv.spec_verify(row, None, i32([[3]]), f([[0.9]]), f([0.999]))
+        assert a.tolist() == [0] and t.tolist() == [[n - 7, -1]]
+        t, a = inv.spec_verify(row * 0, None, i32([[3]]), f([[0.9]]), f([0.999]))
+        assert a.tolist() == [0] and t.tolist() == [[-1, -1]]
     # no weight at all
     z = [[0.0] * V]
     t, a = inv.spec_verify(f([z + z]), None, i32([[0]]), f([[0.0]]), f([0.3]))
