@@ -43,26 +43,14 @@ __device__ __forceinline__ float4 load4(const float* p, int i, int n, float none
   v.w = i + 3 < n ? p[i + 3] : none;
   return v;
 }
-template <bool kVec>
-__device__ __forceinline__ void store4(float* p, int i, int n, float4 v) {
-  if (kVec && i + 3 < n) {
-    *reinterpret_cast<float4*>(p + i) = v;
-    return;
-  }
-  if (i < n) p[i] = v.x;
-  if (i + 1 < n) p[i + 1] = v.y;
-  if (i + 2 < n) p[i + 2] = v.z;
-  if (i + 3 < n) p[i + 3] = v.w;
-}
-
 // ----------------------------------------------------------- softmax_rows ----
 //
 // HBM bound: 8 bytes an element.  Part c of a row (32 THR elements; thread t owns
-// the elements 4t .. 4t+3 of every 4 THR): m_c, s_c = sum exp((x - m_c) t); the row:
-// M = max m_c, S = sum_c s_c exp((m_c - M) t) in ascending c; y = exp((x - m_c) t)
-// (exp((m_c - M) t) / S).  THR and the number of parts follow from n alone, so the
-// order of the sum does too.
-constexpr int kSoftVec = 8;  // float4 a thread
+// every THR-th one from t on: coalesced for any row stride): m_c, s_c = sum exp((x -
+// m_c) t); the row: M = max m_c, S = sum_c s_c exp((m_c - M) t) in ascending c; y =
+// exp((x - m_c) t) (exp((m_c - M) t) / S).  THR and the number of parts follow from n
+// alone, so the order of the sum does too.
+constexpr int kSoftVals = 32;  // elements a thread
 
 template <int THR>
 __device__ __forceinline__ float block_max(float m, float* red) {
@@ -89,43 +77,39 @@ __device__ __forceinline__ float block_sum(float s, float* red) {
   return s;  // valid in lane 0 of every warp
 }
 
-template <int THR, bool kVec>
-__global__ void __launch_bounds__(THR)
+template <int THR>
+__global__ void __launch_bounds__(THR, THR == 256 ? 5 : 1024 / THR)
     softmax_kernel(const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, int* status) {
   __shared__ float red_m[32], red_s[32];
   __shared__ uint64_t parts[kMaxCluster];  // (m_c, s_c)
   const uint32_t rank = cluster_rank(), parts_n = cluster_size();
   cluster_arrive();  // (every CTA of the cluster runs before another stores into it)
   const int64_t r = blockIdx.x / parts_n;
-  const int first = (int)rank * (THR * 4 * kSoftVec);
   const bool in = INV_SPAN_IN_BOUNDS(status, r * ld, r * ld + n - 1, (int64_t)(rows - 1) * ld + n) &&
                   INV_SPAN_IN_BOUNDS(status, r * ld_y, r * ld_y + n - 1, (int64_t)(rows - 1) * ld_y + n);
-  const int n_in = in ? n : 0;
-  const float* xr = x + r * ld;
-  float* yr = y + r * ld_y;
-  float4 v[kSoftVec];
+  const int first = (int)rank * (THR * kSoftVals) + (int)threadIdx.x, left = in ? n - first : 0;  // elements from `first` on
+  const float* xr = x + r * ld + first;
+  float v[kSoftVals];
   float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kSoftVec; ++j) v[j] = load4<kVec>(xr, first + 4 * (int)threadIdx.x + j * 4 * THR, n_in, -INFINITY);
+  for (int j = 0; j < kSoftVals; ++j) v[j] = j * THR < left ? xr[j * THR] : -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kSoftVec; ++j) m = fmaxf(m, fmaxf(fmaxf(v[j].x, v[j].y), fmaxf(v[j].z, v[j].w)));
+  for (int j = 0; j < kSoftVals; ++j) m = fmaxf(m, v[j]);
   m = block_max<THR>(m, red_m);
   const bool none = m == -INFINITY;  // nothing but -inf in this part
-  float s = 0.0f;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int j = 0; j < kSoftVec; ++j) {
-    v[j].x = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].x, m), it));
-    v[j].y = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].y, m), it));
-    v[j].z = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].z, m), it));
-    v[j].w = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j].w, m), it));
-    s = __fadd_rn(s, __fadd_rn(__fadd_rn(v[j].x, v[j].y), __fadd_rn(v[j].z, v[j].w)));
+  for (int j = 0; j < kSoftVals; ++j) {
+    v[j] = none ? 0.0f : expf(__fmul_rn(__fsub_rn(v[j], m), it));
+    s[j & 3] = __fadd_rn(s[j & 3], v[j]);
   }
-  s = block_sum<THR>(s, red_s);
+  const float sc = block_sum<THR>(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])), red_s);
   cluster_wait();
-  if (threadIdx.x == 0) {
-    const uint64_t mine = ((uint64_t)__float_as_uint(s) << 32) | __float_as_uint(m);
-    for (uint32_t q = 0; q < parts_n; ++q) store_cluster(&parts[rank], q, mine);
+  if (threadIdx.x < parts_n) {  // (lane 0's sum goes to every CTA)
+    const float s0 = __shfl_sync((1u << parts_n) - 1u, sc, 0);
+    store_cluster(&parts[rank], threadIdx.x, ((uint64_t)__float_as_uint(s0) << 32) | __float_as_uint(m));
   }
+  __syncwarp();
   cluster_arrive();
   cluster_wait();
   float M = -INFINITY, S = 0.0f;
@@ -135,10 +119,10 @@ __global__ void __launch_bounds__(THR)
     if (mq != -INFINITY) S = __fadd_rn(S, __fmul_rn(sq, expf(__fmul_rn(__fsub_rn(mq, M), it))));
   }
   const float f = none ? 0.0f : __fmul_rn(expf(__fmul_rn(__fsub_rn(m, M), it)), __frcp_rn(S));
+  float* yr = y + r * ld_y + first;
 #pragma unroll
-  for (int j = 0; j < kSoftVec; ++j)
-    store4<kVec>(yr, first + 4 * (int)threadIdx.x + j * 4 * THR, n_in,
-                 make_float4(__fmul_rn(v[j].x, f), __fmul_rn(v[j].y, f), __fmul_rn(v[j].z, f), __fmul_rn(v[j].w, f)));
+  for (int j = 0; j < kSoftVals; ++j)
+    if (j * THR < left) yr[j * THR] = __fmul_rn(v[j], f);
 }
 
 // Rows longer than eight parts: one CTA a row, which reads it three times.
@@ -474,10 +458,9 @@ int launch_clusters(K kernel, int64_t rows, int parts, int threads, cudaStream_t
 }
 
 template <int THR>
-int launch_softmax(bool vec, const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, cudaStream_t s) {
-  const int part = THR * 4 * kSoftVec, parts = (n + part - 1) / part;
-  return launch_clusters(vec ? softmax_kernel<THR, true> : softmax_kernel<THR, false>, rows, parts, THR, s, x, rows, n, ld,
-                         it, y, ld_y, inv::status_ptr());
+int launch_softmax(const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, cudaStream_t s) {
+  const int part = THR * kSoftVals, parts = (n + part - 1) / part;
+  return launch_clusters(softmax_kernel<THR>, rows, parts, THR, s, x, rows, n, ld, it, y, ld_y, inv::status_ptr());
 }
 
 template <int THR>
@@ -498,11 +481,11 @@ int softmax_rows(const float* logits, int rows, int n, int64_t ld, float inv_tem
   if (rows == 0) return INV_OK;
   if (!logits || !probs || (logits == probs && ld != ld_p)) return INV_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = inv::aligned16(logits) && inv::aligned16(probs) && ld % 4 == 0 && ld_p % 4 == 0;
-  // The smallest CTAs whose cluster of at most eight holds a row: many small CTAs overlap their loads, exponentials and
-  // stores (320 rows of 32000: 4 CTAs of 256 threads a row 17.6 us, 1 of 1024 24.9 us).
-  if (n <= kMaxCluster * 256 * 4 * kSoftVec) return launch_softmax<256>(vec, logits, rows, n, ld, inv_temperature, probs, ld_p, s);
-  if (n <= kMaxCluster * 1024 * 4 * kSoftVec) return launch_softmax<1024>(vec, logits, rows, n, ld, inv_temperature, probs, ld_p, s);
+  // The smallest CTAs whose cluster of at most eight holds a row, five a SM: many small CTAs overlap their loads,
+  // exponentials and stores.
+  if (n <= kMaxCluster * 256 * kSoftVals) return launch_softmax<256>(logits, rows, n, ld, inv_temperature, probs, ld_p, s);
+  if (n <= kMaxCluster * 512 * kSoftVals) return launch_softmax<512>(logits, rows, n, ld, inv_temperature, probs, ld_p, s);
+  if (n <= kMaxCluster * 1024 * kSoftVals) return launch_softmax<1024>(logits, rows, n, ld, inv_temperature, probs, ld_p, s);
   softmax_long_kernel<<<(unsigned)rows, kLongThreads, 0, s>>>(logits, rows, n, ld, inv_temperature, probs, ld_p,
                                                               inv::status_ptr());
   INV_CHECK_LAUNCH();
