@@ -27,6 +27,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace {
 
 using inv::record_status;
@@ -472,8 +474,8 @@ __global__ void __launch_bounds__(TH, 2)
 
     // lane r of every warp keeps the state of row r; L and O are per thread: L of rows 2c, 2c + 1 of every n-tile over
     // the warp's keys (the same in all lanes that share c), O of these rows, dims 16 warp + g (+8)
-    const int nrow_r = lane < 8 * NT ? sm.nrow[lane & (8 * NT - 1)] : 0;
-    const float kap_r = lane < 8 * NT ? sm.kappa[lane & (8 * NT - 1)] : 0.0f;
+    const int nrow_r = lane < 8 * NT ? sm.nrow[lane] : 0;
+    const float kap_r = lane < 8 * NT ? sm.kappa[lane] : 0.0f;
     float M_r = -INFINITY, mk_r = -INFINITY;
     int E_r = 0;
     float L[NT][2], o[NT][4];
@@ -527,9 +529,9 @@ __global__ void __launch_bounds__(TH, 2)
       {
         const int seen = min(nrow_r, (b + 1) * BLK);
         if (seen > b * BLK) {
-          float m = sm.red_m[0][lane & (8 * NT - 1)];
+          float m = sm.red_m[0][lane < 8 * NT ? lane : 0];
 #pragma unroll
-          for (int w = 1; w < FEW_WARPS; ++w) m = fmaxf(m, sm.red_m[w][lane & (8 * NT - 1)]);
+          for (int w = 1; w < FEW_WARPS; ++w) m = fmaxf(m, sm.red_m[w][lane < 8 * NT ? lane : 0]);
           M_r = fmaxf(M_r, m);
           const float mk_old = mk_r;
           const int e_old = E_r;
@@ -1384,7 +1386,7 @@ int64_t many_tiles(int T, int n_seqs, int G) { return (int64_t)T / (MANY_ROWS / 
 // effect on the bits.
 struct Plan {
   bool many;       // some sequence may have more than few_tokens new tokens
-  bool direct;     // the tcgen05 kernel folds all segments of a tile itself
+  bool direct;     // a CTA of the tcgen05 kernel takes all segments of its tile and folds them
   int segs;        // else: segments per CTA
   int64_t parts;   // (row, head) pairs with partial results
 };
@@ -1395,11 +1397,25 @@ Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
     if (S == 1) p.parts = 0;
     return p;
   }
-  const int64_t ctas = ((int64_t)T / (MANY_ROWS / G) + 1) * Hkv;
-  p.direct = ctas >= 2 * inv::sm_count() || S == 1;
+  // Direct from two CTAs a SM on: each reads its rows' q once and writes no partial results.
+  const int sms = inv::sm_count();
+  const int64_t tiles = (int64_t)T / (MANY_ROWS / G);
+  p.direct = (tiles + 1) * Hkv >= 2 * sms || S == 1;
   if (p.direct) {
     p.segs = S;
     p.parts = (int64_t)n_seqs * few * Hq;
+    return p;
+  }
+  // Split over keys.  In units of one block of 128 keys (4 us) a CTA costs 2 to start and to finish and 4 per
+  // segment; n CTAs that do not all fit at once take their sum over the SMs and half a CTA's time at the end.
+  // Measured at 32 query and 8 kv heads, 1 / 2 / 4 segments per CTA: 64 tokens over 8192 keys 81 / 72 / 106 us, 512
+  // over 8192 462 / 400 / 408, 512 over 32768 1760 / 1531 / 1403, 32 sequences of 9 over 4096 425 / 376 / 392.
+  const int64_t ctas = std::max<int64_t>(1, std::max<int64_t>(tiles, std::min(n_seqs, T / (few + 1)))) * Hkv;
+  double best = 0.0;
+  for (int segs = 1; segs <= 4; segs *= 2) {
+    const int64_t n = ctas * ((S + segs - 1) / segs);
+    const double one = 2.0 + 4.0 * segs, t = n <= sms ? one : (4.0 * ctas * S + 2.0 * n) / sms + 0.5 * one;
+    if (segs == 1 || t < best) best = t, p.segs = segs;
   }
   return p;
 }
