@@ -510,7 +510,8 @@ INV_API int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads
  *              16-byte aligned (may be NULL if that is 0).  Calls that overlap
  *              on the GPU need separate workspaces.
  * Errors: INV_ERR_INVALID_ARG; INV_ERR_UNSUPPORTED_SHAPE unless head_dim == 128,
- * page_size as above and n_heads / n_kv_heads is an integer from 1 to 16;
+ * page_size as above, n_heads / n_kv_heads is an integer from 1 to 16 and
+ * n_kv_heads <= 65535;
  * INV_ERR_WORKSPACE.  Device: INV_ERR_TIMEOUT, INV_ERR_RANGE (out split
  * overflow).
  */

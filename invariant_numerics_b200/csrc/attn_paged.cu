@@ -1376,7 +1376,9 @@ int allow_smem(F kernel, size_t bytes, bool (&done)[64]) {
   return INV_OK;
 }
 
-int segments(int max_len) { return (max_len + SEG - 1) / SEG; }
+constexpr int MAX_GRID_YZ = 65535;
+
+int segments(int max_len) { return max_len / SEG + (max_len % SEG != 0); }
 
 // Sequences with at most this many new tokens (32 rows) take the mma.sync kernel.
 int few_tokens(int G) { return 32 / G; }
@@ -1417,6 +1419,7 @@ Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
     const double one = 2.0 + 4.0 * segs, t = n <= sms ? one : (4.0 * ctas * S + 2.0 * n) / sms + 0.5 * one;
     if (segs == 1 || t < best) best = t, p.segs = segs;
   }
+  p.segs = std::max(p.segs, (S + MAX_GRID_YZ - 1) / MAX_GRID_YZ);
   return p;
 }
 
@@ -1488,7 +1491,7 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   int rc = inv::check_paged(cache, n_heads);
   if (rc != INV_OK) return rc;
   const int G = n_heads / cache->n_kv_heads;
-  if (G > 16) return INV_ERR_UNSUPPORTED_SHAPE;
+  if (G > 16 || cache->n_kv_heads > MAX_GRID_YZ) return INV_ERR_UNSUPPORTED_SHAPE;
   if (T < 0 || n_seqs < 0 || ld_table < 0 || ld_q < (int64_t)n_heads * D || ld_q % 4 != 0) return INV_ERR_INVALID_ARG;
   if (!(softmax_scale >= 0.0f) || !(softmax_scale <= 1e30f)) return INV_ERR_INVALID_ARG;
   if ((out_hi == nullptr) != (out_lo == nullptr)) return INV_ERR_INVALID_ARG;

@@ -119,3 +119,11 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(inv):
         inv.softmax_rows(z(2, 5))
     with pytest.raises(ValueError, match="CUDA"):
         inv.spec_verify(z(1, 2, 5), None, z(1, 1, dtype=torch.int32), z(1, 1), z(1))
+
+
+def test_the_largest_bounds(inv):
+    """Bounds next to 2^31 keep their sizes positive, and what no launch can hold is refused."""
+    # 4 rows of 32 heads, 2^22 segments of 512 keys, 128 sums and (m, l) each
+    assert inv.lib.attn_paged_workspace_size(4, 2, 32, 8, 0, 2 ** 31 - 1) == 4 * 32 * 2 ** 22 * (128 * 4 + 8)
+    assert attend(inv, ld_table=1 << 40, nb=0) == WORKSPACE
+    assert attend(inv, hq=70000, ld=70000 * 128, c=cache(inv, hkv=70000)) == UNSUPPORTED
