@@ -77,6 +77,12 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr));
 }
 
+// (Volatile: loaded where it is used.)
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t pack_half2(__half lo, __half hi) {
   return (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
 }
@@ -210,15 +216,26 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 //              of an m-tile), the item's rows are the MMA columns.  O^T = V^T W:
 //              warp w owns dims 16w .. 16w+15.  W crosses the warps through shared
 //              memory.
+// Measured (32 query, 8 kv heads): 128 sequences of 2048 keys 246 us (4.45 TB/s of
+// codes, scales and q; the kernel without its products 188), 64 of 8192 307 us.  At
+// one token the warps' instructions (unpacking, W's way through shared memory) and
+// the two barriers a block share the time with HBM; NT = 2 takes 203 us for 32
+// sequences of 4 tokens over 4096 keys, NT = 4 318 us for 5 and 369 us for 8, bound
+// by the MMAs' and the softmax's latency at two CTAs a SM.  Four warps of two m-tiles
+// (264 us for the first case), half-block slots (278) and one CTA a SM with four
+// slots (278; 357 and 408 for 5 and 8 tokens) were slower.
 constexpr int FEW_WARPS = 8, FEW_T = 32 * FEW_WARPS;
 constexpr int TH = FEW_T + 32;
 constexpr int SLOT = BLK * D * 2;  // 32 KB: codes of one block
 constexpr int NST = 2;
 
 // B fragments of 8 rows: lane (g, c) of k-step k holds, for row g, the pairs
-// (16k + 2c, + 1) and (16k + 2c + 8, + 9), hi and lo: {hi0, hi1, lo0, lo1}.
+// (16k + 2c, + 1) and (16k + 2c + 8, + 9).  Eight bytes a lane: with hi and lo side by
+// side the second round's loads of hi alone met every bank twice, and the scattered
+// stores of W four times; shared memory is what the warps wait for most (128 x 2048
+// keys: 250 against 234 us).
 struct Frags {
-  uint4 f[8][32];
+  uint2 hi[8][32], lo[8][32];
 };
 
 // A work item; n_keys = 0: no more.
@@ -372,7 +389,9 @@ __global__ void __launch_bounds__(TH, 2)
   }
 
   // ================================================================ consumers
-  // acc[nt] = sum over 16 x 8 codes of the m-tile at `ldsm(k)`: cross products first, then hi hi
+  // acc[nt] = sum over 16 x 8 codes of the m-tile at `ldsm(k)`: cross products first, then hi hi.  The compiler would
+  // fetch the second round's fragments ahead of the first's end and spill for it; with NT = 4 it does better left alone
+  // in the first (318 / 369 us at 5 / 8 tokens with no fixed place, 325 / 356 with both fixed, 312 / 346 so).
   const auto product = [&](int rows, const Frags* f, float (&acc)[NT][4], auto ldsm) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
@@ -386,9 +405,11 @@ __global__ void __launch_bounds__(TH, 2)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt > 0 && 8 * nt >= rows) break;
-        const uint4 b = f[nt].f[k][lane];
-        mma16816(acc[nt], cl, b.x, b.y);
-        mma16816(acc[nt], ch[k], b.z, b.w);
+        const uint2* ph = &f[nt].hi[k][lane];
+        const uint2* pl = &f[nt].lo[k][lane];
+        const uint2 bh = NT <= 2 ? lds64(inv::smem_u32(ph)) : *ph, bl = NT <= 2 ? lds64(inv::smem_u32(pl)) : *pl;
+        mma16816(acc[nt], cl, bh.x, bh.y);
+        mma16816(acc[nt], ch[k], bl.x, bl.y);
       }
     }
 #pragma unroll
@@ -396,7 +417,7 @@ __global__ void __launch_bounds__(TH, 2)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt > 0 && 8 * nt >= rows) break;
-        const uint2 b = *reinterpret_cast<const uint2*>(&f[nt].f[k][lane]);
+        const uint2 b = lds64(inv::smem_u32(&f[nt].hi[k][lane]));
         mma16816(acc[nt], ch[k], b.x, b.y);
       }
     }
@@ -460,11 +481,13 @@ __global__ void __launch_bounds__(TH, 2)
       inv::split_plain(__fmul_rn(x.z, f), hi[2], lo[2]);
       inv::split_plain(__fmul_rn(x.w, f), hi[3], lo[3]);
       // dims 4 lane, + 1 and + 2, + 3: k-step lane / 4, pairs c = 2 (lane % 2), + 1 of its half (lane % 4) / 2
-      uint32_t* dst = reinterpret_cast<uint32_t*>(&sm.q[r >> 3].f[lane >> 2][4 * (r & 7) + 2 * (lane & 1)]) + ((lane >> 1) & 1);
-      dst[0] = pack_half2(hi[0], hi[1]);
-      dst[2] = pack_half2(lo[0], lo[1]);
-      dst[4] = pack_half2(hi[2], hi[3]);
-      dst[6] = pack_half2(lo[2], lo[3]);
+      const int k = lane >> 2, at = 4 * (r & 7) + 2 * (lane & 1), word = (lane >> 1) & 1;
+      uint32_t* dh = reinterpret_cast<uint32_t*>(&sm.q[r >> 3].hi[k][at]) + word;
+      uint32_t* dl = reinterpret_cast<uint32_t*>(&sm.q[r >> 3].lo[k][at]) + word;
+      dh[0] = pack_half2(hi[0], hi[1]);
+      dh[2] = pack_half2(hi[2], hi[3]);
+      dl[0] = pack_half2(lo[0], lo[1]);
+      dl[2] = pack_half2(lo[2], lo[3]);
       if (lane == 0) {
         sm.kappa[r] = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
         sm.nrow[r] = r < rows ? min(SEG, it.pos0 + r / G + 1 - key0) : 0;
@@ -546,7 +569,8 @@ __global__ void __launch_bounds__(TH, 2)
       for (int nt = 0; nt < NT; ++nt) {
         if (nt > 0 && 8 * nt >= rows) break;
         const float2 kap2 = *reinterpret_cast<const float2*>(&sm.kappa[8 * nt + 2 * c]);
-        __half* wf = reinterpret_cast<__half*>(&sm.w[nt].f[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
+        __half* wh = reinterpret_cast<__half*>(&sm.w[nt].hi[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
+        __half* wl = reinterpret_cast<__half*>(&sm.w[nt].lo[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int src = 8 * nt + 2 * c + i;
@@ -566,11 +590,10 @@ __global__ void __launch_bounds__(TH, 2)
           __half h0, l0, h1, l1;
           inv::split_plain(w0, h0, l0);
           inv::split_plain(w1, h1, l1);
-          __half* d = wf + i * 32;  // row 2c + i: lane 4 (2c + i) + g / 2
-          d[0] = h0;
-          d[2] = h1;
-          d[4] = l0;
-          d[6] = l1;
+          wh[16 * i] = h0;  // row 2c + i: lane 4 (2c + i) + g / 2
+          wh[16 * i + 2] = h1;
+          wl[16 * i] = l0;
+          wl[16 * i + 2] = l1;
           float s = __fadd_rn(p0, p1);
           s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 8));
           s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 16));
@@ -657,8 +680,13 @@ __global__ void __launch_bounds__(TH, 2)
 //               page numbers the converters need.
 // Tensor memory (512 columns): Q hi | Q lo (64 each), two score blocks (128
 // each, W in place of the scores), O (128).
-// Each product is three MMAs (hi lo, lo hi, hi hi): 3 x 2 x 128 x 128 x 128
-// multiply-adds a block, 3072 clocks at the tensor core's rate, is the bound.
+// Each product is three chains of 8 MMAs (hi lo, lo hi, hi hi) of 64 clocks, two
+// products a block.  Measured: a prompt of 8192 tokens (32 query, 8 kv heads) 2.26 ms,
+// 243 TFLOP/s of useful products and three times that executed, 0.44 of the dense
+// rate.  Two chains of about 8K clocks a block bound it, which overlap each other
+// and the MMAs: the softmax warps', and unpacking V with the product behind it.
+// 16 softmax warps (2.70 ms), separate converters for K and V (2.43) and folding O
+// in before the weights (2.30) were slower.
 // The roles' loops are kept rolled and each step is written once: unrolled and
 // inlined twice they were 34 KB of instructions a block, more than the SM's
 // instruction cache holds, and every step ran four times slower.
