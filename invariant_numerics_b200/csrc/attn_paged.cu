@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -204,7 +205,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 // ------------------------------------------------------- few rows: mma.sync --
 //
 // Persistent CTAs (two a SM), each taking every gridDim.x-th work item = (sequence
-// of at most 8 NT rows, segment, kv head); a row is a (token, query head of the
+// of at most 32 rows, segment, kv head); a row is a (token, query head of the
 // group) pair.  Bound by HBM: 520 bytes a key and kv head.
 //   warp 8     producer: reads an item's descriptors and page numbers, brings its
 //              scales (bulk copies) and its K and V blocks of 128 keys (2-D TMA,
@@ -216,14 +217,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 //              of an m-tile), the item's rows are the MMA columns.  O^T = V^T W:
 //              warp w owns dims 16w .. 16w+15.  W crosses the warps through shared
 //              memory.
-// Measured (32 query, 8 kv heads): 128 sequences of 2048 keys 246 us (4.45 TB/s of
-// codes, scales and q; the kernel without its products 188), 64 of 8192 307 us.  At
-// one token the warps' instructions (unpacking, W's way through shared memory) and
-// the two barriers a block share the time with HBM; NT = 2 takes 203 us for 32
-// sequences of 4 tokens over 4096 keys, NT = 4 318 us for 5 and 369 us for 8, bound
-// by the MMAs' and the softmax's latency at two CTAs a SM.  Four warps of two m-tiles
-// (264 us for the first case), half-block slots (278) and one CTA a SM with four
-// slots (278; 357 and 408 for 5 and 8 tokens) were slower.
+// An item is computed by the code for its number of tiles of 8 rows, so a decode row
+// in a call with prompts or drafts costs what it costs alone (128 x 2048 keys 235 us;
+// with the code of four tiles 527, with its idle tiles skipped at run time 361).
+// Measured (32 query, 8 kv heads): 128 sequences of 2048 keys 232 us (4.73 TB/s of
+// codes, scales and q; without its products 188), 64 of up to 8192 289 us; 32
+// sequences over 4096 keys: 4 tokens 183, 5 tokens 237, 8 tokens 297.  Not HBM but the
+// warps bound it: loads from shared memory, unpacking, two barriers a block; from
+// three tiles on the MMAs' and the softmax's latency too, at two CTAs a SM.  Four warps
+// of two m-tiles (264 us for the first case), half-block slots (278) and one CTA a SM
+// with four slots (278) were slower.
+constexpr int MAX_NT = 4;  // tiles of 8 rows of an item
 constexpr int FEW_WARPS = 8, FEW_T = 32 * FEW_WARPS;
 constexpr int TH = FEW_T + 32;
 constexpr int SLOT = BLK * D * 2;  // 32 KB: codes of one block
@@ -243,16 +247,15 @@ struct Item {
   int seq, row0, n_new, pos0, seg, h, n_keys;
 };
 
-template <int NT>
 struct __align__(1024) FewSmem {
   uint8_t ring[NST * SLOT];
-  Frags q[NT], w[NT];
+  Frags q[MAX_NT], w[MAX_NT];
   float ks[2][SEG], vs[2][SEG];  // scales of this and the next item (unspecified behind their last key)
   float pm[SEG];                 // running maximum of vs
-  float red_m[FEW_WARPS][8 * NT];
-  float red_l[FEW_WARPS][8 * NT];
-  float kappa[8 * NT];
-  int nrow[8 * NT];  // keys of the row in the segment (may be <= 0)
+  float red_m[FEW_WARPS][8 * MAX_NT];
+  float red_l[FEW_WARPS][8 * MAX_NT];
+  float kappa[8 * MAX_NT];
+  int nrow[8 * MAX_NT];  // keys of the row in the segment (may be <= 0)
   Item item[2];
   uint64_t full[NST], empty[NST], item_full[2], item_empty[2];
   int abort;
@@ -281,7 +284,7 @@ __device__ __forceinline__ void few_sync() { asm volatile("barrier.cta.sync 1, %
 
 // kLast: the fold is not launched (no sequence has a second segment); the item's
 // results are the rows' outputs.
-template <int NT, bool kLast>
+template <bool kLast>
 __global__ void __launch_bounds__(TH, 2)
     attn_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ AttnArgs a) {
@@ -289,8 +292,7 @@ __global__ void __launch_bounds__(TH, 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int G = a.G, Hkv = a.c.n_kv_heads;
   extern __shared__ uint8_t smem_raw[];
-  using Smem = FewSmem<NT>;
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FewSmem& sm = *reinterpret_cast<FewSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       inv::mbar_init(&sm.full[i], 1);
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(TH, 2)
       const int64_t rest = id / Hkv;
       it.seg = (int)(rest % a.S_max);
       Tile t;
-      if (!load_seq(a, (int)(rest / a.S_max), lane, t) || t.n_new > a.few || t.n_new * G > 8 * NT) continue;
+      if (!load_seq(a, (int)(rest / a.S_max), lane, t) || t.n_new > a.few || t.n_new * G > 8 * MAX_NT) continue;
       const int key0 = it.seg * SEG;
       it.seq = t.seq;
       it.row0 = t.row0;
@@ -390,11 +392,13 @@ __global__ void __launch_bounds__(TH, 2)
 
   // ================================================================ consumers
   // acc[nt] = sum over 16 x 8 codes of the m-tile at `ldsm(k)`: cross products first, then hi hi.  The compiler would
-  // fetch the second round's fragments ahead of the first's end and spill for it; with NT = 4 it does better left alone
-  // in the first (318 / 369 us at 5 / 8 tokens with no fixed place, 325 / 356 with both fixed, 312 / 346 so).
-  const auto product = [&](int rows, const Frags* f, float (&acc)[NT][4], auto ldsm) {
+  // keep the first round's fragments for the second, or fetch these early, and spill for it: the second round's loads
+  // are volatile (4 tokens 203 -> 175 us).  In the first round only one tile gains by that (238 -> 234 us; more tiles
+  // lose up to 20 %).
+  const auto product = [&](const Frags* f, auto& acc, auto ldsm) {
+    constexpr int N = sizeof(acc) / sizeof(acc[0]);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+    for (int nt = 0; nt < N; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
     uint32_t ch[8][4];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -403,11 +407,10 @@ __global__ void __launch_bounds__(TH, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) inv::unpack_code(w[i], ch[k][i], cl[i]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0 && 8 * nt >= rows) break;
+      for (int nt = 0; nt < N; ++nt) {
         const uint2* ph = &f[nt].hi[k][lane];
         const uint2* pl = &f[nt].lo[k][lane];
-        const uint2 bh = NT <= 2 ? lds64(inv::smem_u32(ph)) : *ph, bl = NT <= 2 ? lds64(inv::smem_u32(pl)) : *pl;
+        const uint2 bh = N == 1 ? lds64(inv::smem_u32(ph)) : *ph, bl = N == 1 ? lds64(inv::smem_u32(pl)) : *pl;
         mma16816(acc[nt], cl, bh.x, bh.y);
         mma16816(acc[nt], ch[k], bl.x, bl.y);
       }
@@ -415,8 +418,7 @@ __global__ void __launch_bounds__(TH, 2)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0 && 8 * nt >= rows) break;
+      for (int nt = 0; nt < N; ++nt) {
         const uint2 b = lds64(inv::smem_u32(&f[nt].hi[k][lane]));
         mma16816(acc[nt], ch[k], b.x, b.y);
       }
@@ -426,20 +428,16 @@ __global__ void __launch_bounds__(TH, 2)
   const int kk0 = 16 * warp + g;  // this lane's keys in a block: kk0, kk0 + 8
   uint32_t n_slot = 0;
 
-#pragma unroll 1
-  for (uint32_t n_item = 0;; ++n_item) {
-    const int ab = n_item & 1;
-    ok = bar_wait<true>(&sm.item_full[ab], (n_item >> 1) & 1, a, &sm.abort) && ok;
-    if (few_sync_any(!ok)) break;
-    const Item it = sm.item[ab];
-    if (it.n_keys == 0) break;
+  // One item with its rows in N tiles of 8 columns; false: a wait gave up.
+  const auto run_item = [&](auto tiles, const Item& it, int ab) -> bool {
+    constexpr int N = decltype(tiles)::value;
     const int rows = it.n_new * G, key0 = it.seg * SEG, nblk = (it.n_keys + BLK - 1) / BLK;
     const float* ks = sm.ks[ab];
     const float* vs = sm.vs[ab];
     // the rows' q, scaled by 2^e and split; lane holds dims 4 lane .. 4 lane + 3
-    float4 qx[NT];
+    float4 qx[N];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int r = warp + FEW_WARPS * i, tok = r / G;
       qx[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
@@ -467,7 +465,7 @@ __global__ void __launch_bounds__(TH, 2)
       *reinterpret_cast<float2*>(sm.pm + j) = make_float2(p0, fmaxf(p0, s1));
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int r = warp + FEW_WARPS * i;
       const float4 x = qx[i];
       float m = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
@@ -497,13 +495,13 @@ __global__ void __launch_bounds__(TH, 2)
 
     // lane r of every warp keeps the state of row r; L and O are per thread: L of rows 2c, 2c + 1 of every n-tile over
     // the warp's keys (the same in all lanes that share c), O of these rows, dims 16 warp + g (+8)
-    const int nrow_r = lane < 8 * NT ? sm.nrow[lane] : 0;
-    const float kap_r = lane < 8 * NT ? sm.kappa[lane] : 0.0f;
+    const int nrow_r = lane < 8 * N ? sm.nrow[lane] : 0;
+    const float kap_r = lane < 8 * N ? sm.kappa[lane] : 0.0f;
     float M_r = -INFINITY, mk_r = -INFINITY;
     int E_r = 0;
-    float L[NT][2], o[NT][4];
+    float L[N][2], o[N][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < N; ++nt) {
       L[nt][0] = L[nt][1] = 0.0f;
       o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.0f;
     }
@@ -513,10 +511,10 @@ __global__ void __launch_bounds__(TH, 2)
     for (int b = 0; b < nblk; ++b) {
       // ----------------------------------------------------------- scores --
       ok = bar_wait<true>(&sm.full[n_slot % NST], (n_slot / NST) & 1, a, &sm.abort) && ok;
-      float x[NT][4];  // keys kk0 (+8), rows 2c, 2c + 1
+      float x[N][4];  // keys kk0 (+8), rows 2c, 2c + 1
       {
         const uint32_t kb = ring + (n_slot % NST) * SLOT;
-        product(rows, sm.q, x, [&](int k, uint32_t (&w)[4]) {
+        product(sm.q, x, [&](int k, uint32_t (&w)[4]) {
           ldsm_x4(code_addr(kb, 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), 16 * k + (lane >> 4) * 8), w);
         });
       }
@@ -526,8 +524,7 @@ __global__ void __launch_bounds__(TH, 2)
       const int key = b * BLK + kk0;
       const float k0 = ks[key], k1 = ks[key + 8];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0 && 8 * nt >= rows) break;
+      for (int nt = 0; nt < N; ++nt) {
         float mx[2];
         const int2 nr = *reinterpret_cast<const int2*>(&sm.nrow[8 * nt + 2 * c]);
 #pragma unroll
@@ -552,9 +549,9 @@ __global__ void __launch_bounds__(TH, 2)
       {
         const int seen = min(nrow_r, (b + 1) * BLK);
         if (seen > b * BLK) {
-          float m = sm.red_m[0][lane < 8 * NT ? lane : 0];
+          float m = sm.red_m[0][lane < 8 * N ? lane : 0];
 #pragma unroll
-          for (int w = 1; w < FEW_WARPS; ++w) m = fmaxf(m, sm.red_m[w][lane < 8 * NT ? lane : 0]);
+          for (int w = 1; w < FEW_WARPS; ++w) m = fmaxf(m, sm.red_m[w][lane < 8 * N ? lane : 0]);
           M_r = fmaxf(M_r, m);
           const float mk_old = mk_r;
           const int e_old = E_r;
@@ -566,8 +563,7 @@ __global__ void __launch_bounds__(TH, 2)
       }
       const float v0 = vs[key], v1 = vs[key + 8];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0 && 8 * nt >= rows) break;
+      for (int nt = 0; nt < N; ++nt) {
         const float2 kap2 = *reinterpret_cast<const float2*>(&sm.kappa[8 * nt + 2 * c]);
         __half* wh = reinterpret_cast<__half*>(&sm.w[nt].hi[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
         __half* wl = reinterpret_cast<__half*>(&sm.w[nt].lo[warp][4 * (2 * c) + (g >> 1)]) + (g & 1);
@@ -607,13 +603,12 @@ __global__ void __launch_bounds__(TH, 2)
       ok = bar_wait<true>(&sm.full[n_slot % NST], (n_slot / NST) & 1, a, &sm.abort) && ok;
       {
         const uint32_t vb = ring + (n_slot % NST) * SLOT;
-        product(rows, sm.w, x, [&](int k, uint32_t (&w)[4]) {
+        product(sm.w, x, [&](int k, uint32_t (&w)[4]) {
           ldsm_x4_t(code_addr(vb, 16 * k + (lane >> 4) * 8 + (lane & 7), 16 * warp + ((lane >> 3) & 1) * 8), w);
         });
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (nt > 0 && 8 * nt >= rows) break;
-          const float b0 = __shfl_sync(0xffffffffu, beta_r, 8 * nt + 2 * c), b1 = __shfl_sync(0xffffffffu, beta_r, 8 * nt + 2 * c + 1);
+        for (int nt = 0; nt < N; ++nt) {
+            const float b0 = __shfl_sync(0xffffffffu, beta_r, 8 * nt + 2 * c), b1 = __shfl_sync(0xffffffffu, beta_r, 8 * nt + 2 * c + 1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[nt][i] = __fmaf_rn(o[nt][i], (i & 1) ? b1 : b0, x[nt][i]);
         }
@@ -622,17 +617,17 @@ __global__ void __launch_bounds__(TH, 2)
       warp_arrive(&sm.empty[n_slot % NST], lane);
       ++n_slot;
     }
-    if (gone) break;
+    if (gone) return false;
 
     // ------------------------------------------------------ segment results --
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < N; ++nt)
       if (g == 0) *reinterpret_cast<float2*>(&sm.red_l[warp][8 * nt + 2 * c]) = make_float2(L[nt][0], L[nt][1]);
     inv::fence_proxy_async_smem();  // the scales' reads before the next copy into their buffer
     warp_arrive(&sm.item_empty[ab], lane);
     few_sync();
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < N; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * nt + 2 * c + i, tok = r / G, head = it.h * G + (r - tok * G);
@@ -660,6 +655,26 @@ __global__ void __launch_bounds__(TH, 2)
           if (warp == 0 && g == 0) a.part_ml[rs] = make_float2(mk, l);
         }
       }
+    return true;
+  };
+#pragma unroll 1
+  for (uint32_t n_item = 0;; ++n_item) {
+    const int ab = n_item & 1;
+    ok = bar_wait<true>(&sm.item_full[ab], (n_item >> 1) & 1, a, &sm.abort) && ok;
+    if (few_sync_any(!ok)) break;
+    const Item it = sm.item[ab];
+    if (it.n_keys == 0) break;
+    const int tiles = (it.n_new * G + 7) >> 3;
+    bool more;
+    if (tiles == 1)
+      more = run_item(std::integral_constant<int, 1>{}, it, ab);
+    else if (tiles == 2)
+      more = run_item(std::integral_constant<int, 2>{}, it, ab);
+    else if (tiles == 3)
+      more = run_item(std::integral_constant<int, 3>{}, it, ab);
+    else
+      more = run_item(std::integral_constant<int, MAX_NT>{}, it, ab);
+    if (!more) break;
   }
 }
 
@@ -1408,8 +1423,10 @@ constexpr int MAX_GRID_YZ = 65535;
 
 int segments(int max_len) { return max_len / SEG + (max_len % SEG != 0); }
 
-// Sequences with at most this many new tokens (32 rows) take the mma.sync kernel.
-int few_tokens(int G) { return 32 / G; }
+// Sequences with at most this many new tokens (32 rows) take the mma.sync kernel: at 32
+// sequences over 4096 keys, 5 tokens of 4 heads (20 rows) take it 237 us and the tcgen05
+// kernel 391, 8 tokens (32 rows) 297 and 373.
+int few_tokens(int G) { return 8 * MAX_NT / G; }
 int64_t many_tiles(int T, int n_seqs, int G) { return (int64_t)T / (MANY_ROWS / G) + n_seqs; }
 
 // How a call's work is cut: by its sizes and bounds only, and without any
@@ -1451,14 +1468,14 @@ Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
   return p;
 }
 
-template <int NT, bool kLast>
+template <bool kLast>
 int launch_few(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   static bool done[64] = {};
-  constexpr size_t smem = sizeof(FewSmem<NT>) + 1024;
-  const int rc = allow_smem(attn_few_kernel<NT, kLast>, smem, done);
+  constexpr size_t smem = sizeof(FewSmem) + 1024;
+  const int rc = allow_smem(attn_few_kernel<kLast>, smem, done);
   if (rc != INV_OK) return rc;
   const int64_t items = (int64_t)a.rb.n_seqs * a.S_max * a.c.n_kv_heads, fit = 2 * inv::sm_count();
-  attn_few_kernel<NT, kLast><<<(unsigned)(items < fit ? items : fit), TH, smem, s>>>(tk, tv, a);
+  attn_few_kernel<kLast><<<(unsigned)(items < fit ? items : fit), TH, smem, s>>>(tk, tv, a);
   INV_CHECK_LAUNCH();
   return INV_OK;
 }
@@ -1568,14 +1585,8 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
                                CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != INV_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int rows = (a.max_q < a.few ? a.max_q : a.few) * G;
   const bool last = !p.many && a.S_max == 1;  // no fold
-  if (rows <= 8)
-    rc = last ? launch_few<1, true>(a, tk, tv, s) : launch_few<1, false>(a, tk, tv, s);
-  else if (rows <= 16)
-    rc = last ? launch_few<2, true>(a, tk, tv, s) : launch_few<2, false>(a, tk, tv, s);
-  else
-    rc = last ? launch_few<4, true>(a, tk, tv, s) : launch_few<4, false>(a, tk, tv, s);
+  rc = last ? launch_few<true>(a, tk, tv, s) : launch_few<false>(a, tk, tv, s);
   if (rc == INV_OK && p.many) rc = p.direct ? launch_many<true>(a, s) : launch_many<false>(a, s);
   if (rc != INV_OK) return rc;
   return last ? INV_OK : launch_fold(a, s);
