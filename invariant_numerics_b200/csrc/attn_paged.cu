@@ -3,7 +3,9 @@
 //
 // Row arithmetic (the same operations, in the same order, whatever kernel,
 // tile or split a row is computed in):
-//   q_s = q 2^e with max |q_s| in [2^13, 2^14), q_s = q_hi + q_lo in binary16;
+//   q_s = q 2^e with max |q_s| in [2^13, 2^14), q_s = q_hi + q_lo in binary16
+//            (off by 2^-22 |q_s|, or 2^-25 where q_lo is subnormal: 2^-38 of the row's
+//            largest value; the same holds for w below);
 //   code / 2 = c_hi + c_lo (unpack_code, exact, c_hi = rn16(code / 2));
 //   acc_j  = fp32 tensor-core sum over d in steps of 16: first, per step,
 //            c_lo q_hi and c_hi q_lo, then a second round of c_hi q_hi (the
@@ -1540,7 +1542,8 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   if (T < 0 || n_seqs < 0 || ld_table < 0 || ld_q < (int64_t)n_heads * D || ld_q % 4 != 0) return INV_ERR_INVALID_ARG;
   if (!(softmax_scale >= 0.0f) || !(softmax_scale <= 1e30f)) return INV_ERR_INVALID_ARG;
   if ((out_hi == nullptr) != (out_lo == nullptr)) return INV_ERR_INVALID_ARG;
-  if (T == 0 || n_seqs == 0 || ld_table == 0) return INV_OK;
+  if (T == 0 || n_seqs == 0) return INV_OK;
+  if (ld_table == 0) return INV_ERR_INVALID_ARG;  // no sequence of the call could have a key
   if (!q || !page_table || !q_start || !len || !out || !cache->k || !cache->v || !cache->k_scale || !cache->v_scale)
     return INV_ERR_INVALID_ARG;
   if (!inv::aligned16(q) || !inv::aligned16(out) || !inv::aligned16(cache->k) || !inv::aligned16(cache->v) ||

@@ -82,7 +82,12 @@ def attend_bound(q, cache, table, start, lens, scale=SCALE):
     A product x c of a fp32 value x (a query value, a weight) and a code c is formed from two binary16 parts of each:
     x up to 2^-22 |x|, c exactly, and the product of the low parts (2^-11 each) is dropped; 24 accumulations at 2^-24
     of the sum of |x c|: below 2^-19 together.  A score's error moves its weight by that relative amount (2^-18 for
-    the exponential, the scalings and the joins), and the normaliser by the weighted mean of them."""
+    the exponential, the scalings and the joins), and the normaliser by the weighted mean of them.
+
+    A weight p_j s_j is split after a scaling 2^E with 2^E s in [2^13, 2^14) for the largest scale s among the row's
+    keys, so its low part is a multiple of 2^-24 and off by up to 2^-25 where the weight is far below the largest: by
+    2^-25 2^-E <= 2^-38 s, times |code_j|, over a normaliser of at least 1 - 2^-18 (the largest p is 1): 2^-37 s
+    sum_j |code_j|.  It shows where the keys that carry the weight have code 0."""
     out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
     G = q.shape[1] // cache.n_kv_heads
     st, ln = start.tolist(), lens.tolist()
@@ -98,7 +103,11 @@ def attend_bound(q, cache, table, start, lens, scale=SCALE):
             err = scale * 2.0 ** -19 * torch.einsum("rgd,kd->rgk", qq.abs(), k.abs()) + 2.0 ** -18
             w = torch.softmax(t, -1)
             e = (w * err).sum(-1, keepdim=True)
-            out[st[i]:st[i + 1], h * G:(h + 1) * G] = torch.einsum("rgk,kd->rgd", w * (err + e + 2.0 ** -19), v.abs())
+            pg = table[i, :-(-n // cache.page_size)].long()
+            s = cache.v_scale[pg, h].double().flatten()[:n].cummax(0).values[n - m:]
+            c = cache.v[pg, h].double().abs().flatten(0, 1)[:n].cumsum(0)[n - m:]
+            out[st[i]:st[i + 1], h * G:(h + 1) * G] = 2.0 ** -37 * (s[:, None] * c)[:, None] + torch.einsum(
+                "rgk,kd->rgd", w * (err + e + 2.0 ** -19), v.abs())
     return out
 
 
@@ -192,6 +201,30 @@ def test_attn_paged_large_batch_equals_its_parts(inv):
         assert torch.equal(got, full[a:a + count]), (i, first, count)
     again = inv.attn_paged(q, cache, table, start, ln, SCALE)
     assert torch.equal(again, full) and status() == inv.INV_OK
+
+
+@pytest.mark.parametrize("hq,hkv,page,long", [(32, 8, 16, 1400), (32, 8, 64, 500), (16, 1, 32, 1100)])
+def test_attn_paged_mixed_token_counts(inv, hq, hkv, page, long):
+    """More work items than fit the GPU at once, sequences of 1, 2, .. new tokens in turn: each as if alone."""
+    news = [1 + i % 9 for i in range(45)]
+    r = np.random.default_rng(long)
+    lens = [int(n + r.integers(0, long)) for n in news]
+    n_pages, table, start, ln = batch(lens, news, page, seed=61)
+    cache = pool(inv, n_pages, hkv, page, seed=62)
+    q = torch.randn(int(start[-1]), hq, 128, generator=gen(63), device="cuda")
+    few = [i for i in range(45) if news[i] <= 8]  # without the sequences of 9 tokens too
+    st = start.tolist()
+    rows = torch.cat([torch.arange(st[i], st[i + 1]) for i in few]).cuda()
+    full = inv.attn_paged(q, cache, table, start, ln, SCALE)
+    part = inv.attn_paged(q[rows], cache, table[few].contiguous(),
+                          i32(np.concatenate([[0], np.cumsum([news[i] for i in few])]).tolist()),
+                          i32([lens[i] for i in few]), SCALE, max_q_bound=8)
+    assert torch.equal(part, full[rows])
+    for i in range(0, 45, 4):
+        got = inv.attn_paged(q[st[i]:st[i + 1]], cache, table[i:i + 1], i32([0, news[i]]), ln[i:i + 1], SCALE)
+        assert torch.equal(got, full[st[i]:st[i + 1]]), (i, news[i])
+    check_attend(inv, q, cache, table, start, ln, full)
+    assert status() == inv.INV_OK
 
 
 def test_attn_paged_unused_memory_does_not_matter(inv):

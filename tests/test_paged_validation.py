@@ -126,4 +126,5 @@ def test_the_largest_bounds(inv):
     # 4 rows of 32 heads, 2^22 segments of 512 keys, 128 sums and (m, l) each
     assert inv.lib.attn_paged_workspace_size(4, 2, 32, 8, 0, 2 ** 31 - 1) == 4 * 32 * 2 ** 22 * (128 * 4 + 8)
     assert attend(inv, ld_table=1 << 40, nb=0) == WORKSPACE
+    assert attend(inv, ld_table=0) == INVALID and attend(inv, ld_table=0, T=0) == OK
     assert attend(inv, hq=70000, ld=70000 * 128, c=cache(inv, hkv=70000)) == UNSUPPORTED
