@@ -268,7 +268,6 @@ def _verify(s):
     else:
         i = x.gather(1, k.clamp_max(d - 1)[:, None])
         w.scatter_(1, i, torch.where((k < d)[:, None], torch.zeros_like(px[:, :1]), w.gather(1, i)))
-    w = torch.where(w.sum(1, keepdim=True) > 0, w, p[rows, k].double())
     c = w.cumsum(1)
     hit = (c > s["u_sample"].double()[:, None] * c[:, -1:]) & (w > 0)
     new = hit.to(torch.uint8).argmax(1)
@@ -399,7 +398,7 @@ def _exact_verify(s):
             left = torch.relu(left - s["draft"][i, k].double().cpu())
         elif k < d:
             left[drafted[i][k]] = 0.0
-        sums = (left if left.max() > 0 else s["target"][i, k].double().cpu()).cumsum(0)
+        sums = left.cumsum(0)
         tokens[i, k] = torch.searchsorted(sums, float(s["u_sample"][i]) * sums[-1], right=True)
         accepted[i] = k
     return {"tokens": tokens, "accepted": accepted}
