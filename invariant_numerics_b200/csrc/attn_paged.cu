@@ -718,7 +718,7 @@ static_assert(SOFT_REGS >= MANY_REGS && CONV_REGS <= MANY_REGS && REST_REGS <= M
 static_assert(SOFT_T * SOFT_REGS + CONV_T * CONV_REGS + 128 * REST_REGS <= MANY_T * MANY_REGS, "registers of the CTA");
 constexpr int OPER = BLK * D * 2;  // bytes of one binary16 operand (hi or lo) of a block
 constexpr uint32_t COL_QH = 0, COL_QL = 64, COL_S = 128, COL_O = 384;
-constexpr int PAGE_RING = 8, PAGE_AHEAD = 3;  // blocks of page numbers held, and written ahead of the scales
+constexpr int PAGE_RING = 16, PAGE_AHEAD = 3;  // blocks of page numbers held, and written ahead of the scales
 
 struct __align__(1024) ManySmem {
   uint8_t k[2 * OPER];  // hi, lo; [d half][key][64], 128-byte swizzle
@@ -1254,8 +1254,10 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
     if (warp == SCALE_WARP) {
     // ================================================================= scales
     float carry = 0.0f;  // largest V scale of the segment so far
-    // Page numbers of block j.  Its slot held block j - 8's, whose V was loaded before K of block j - 7 was stored:
-    // before the softmax of block j - 7 <= i - 4.
+    // Page numbers of block j, behind the softmax of block j - 7.  A converter warp reads those of block m last for the
+    // second half of its V, which it loads after it has passed on K of block m + 1 and before it passes on K of block
+    // m + 2.  So the softmax of block m + 2 is behind these reads, that of block m + 1 is not: the slot may hold pages
+    // of block j - 9 and older (tests/test_paged_pipeline.py checks the order of all roles).
     const auto put_pages = [&](int j) {
       if (lane < BLK / 16) {
         const int key = (b0 + j) * BLK + 16 * lane;
