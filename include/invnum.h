@@ -442,10 +442,12 @@ INV_API int prefill_layer(const inv_layer_config* cfg, const inv_layer_weights* 
  *             (not read for a sequence without new tokens).
  *   page_table : int32 [n_seqs][ld_table]; only the entries of the positions
  *             0 .. len[i] - 1 are read.
- * A sequence whose len is smaller than its number of new tokens or beyond the
- * call's bounds, and a page number outside the cache, record
- * INV_ERR_INVALID_ARG; the rows concerned are skipped (attn_paged: a row that
- * reaches a bad page gets unspecified finite values).
+ * A sequence whose q_start entries lie outside 0 .. T or descend, one whose len
+ * is smaller than its number of new tokens or beyond the call's bounds, and a
+ * page number outside the cache, record INV_ERR_INVALID_ARG; the rows concerned
+ * are skipped (attn_paged: a row that reaches a bad page gets unspecified finite
+ * values).  Where q_start descends, which sequence a row belongs to is not
+ * defined: any row of the call may be skipped or get unspecified values.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int16_t* k;

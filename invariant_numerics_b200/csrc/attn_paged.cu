@@ -133,13 +133,18 @@ __device__ __forceinline__ int64_t part_index(const AttnArgs& a, int seq, int to
   return (a.by_seq ? (int64_t)a.rb.n_seqs * a.few : (int64_t)a.T) * a.Hq * a.S_max;
 }
 
-// Checks sequence i's descriptors; fills everything but the tile's tokens.
+// Checks sequence i's descriptors; fills everything but the tile's tokens.  The
+// mma.sync kernel looks at every sequence of a call and records a wrong q_start;
+// the other kernels only skip it (recording it there too cost the tcgen05 kernel
+// registers: 276 bytes of spill loads against 208).
+template <bool kRecordRows = false>
 __device__ __forceinline__ bool load_seq(const AttnArgs& a, int i, int lane, Tile& t) {
   const int q0 = a.rb.q_start[i], q1 = a.rb.q_start[i + 1];
+  if (kRecordRows && lane == 0 && (q0 < 0 || q1 < q0 || q1 > a.T)) record_status(a.status, INV_ERR_INVALID_ARG);
+  if (q0 < 0 || q1 <= q0 || q1 > a.T) return false;
   t.seq = i;
   t.row0 = q0;
   t.n_new = q1 - q0;
-  if (q0 < 0 || q1 > a.T || t.n_new <= 0) return false;
   t.len = a.rb.len[i];
   if (t.n_new > a.max_q || t.len < t.n_new || t.len > a.max_len) {
     if (lane == 0) record_status(a.status, INV_ERR_INVALID_ARG);
@@ -150,12 +155,14 @@ __device__ __forceinline__ bool load_seq(const AttnArgs& a, int i, int lane, Til
 
 // Tiles are numbered so that sequence i owns the ids q_start[i] / per + i ..:
 // ascending in i and never overlapping (floor((a + n) / per) + 1 - floor(a /
-// per) >= ceil(n / per)), without a pass over the batch.  False: no such tile.
+// per) >= ceil(n / per)), without a pass over the batch.  False: no such tile (where
+// q_start descends, the search may end at a sequence whose ids begin behind id).
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, int lane, Tile& t) {
   const int i = inv::warp_upper(a.rb.n_seqs, id, lane, [&](int j) { return a.rb.q_start[j] / per + j; });
   if (i < 0 || !load_seq(a, i, lane, t)) return false;
-  t.tok0 = (id - (t.row0 / per + i)) * per;
-  if (t.tok0 >= t.n_new) return false;
+  const int j = id - (t.row0 / per + i);
+  if (j < 0 || j > (t.n_new - 1) / per) return false;
+  t.tok0 = j * per;
   t.ntok = min(per, t.n_new - t.tok0);
   t.row0 += t.tok0;
   return true;
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(TH, 2)
       const int64_t rest = id / Hkv;
       it.seg = (int)(rest % a.S_max);
       Tile t;
-      if (!load_seq(a, (int)(rest / a.S_max), lane, t) || t.n_new > a.few || t.n_new * G > 8 * MAX_NT) continue;
+      if (!load_seq<true>(a, (int)(rest / a.S_max), lane, t) || t.n_new > a.few || t.n_new * G > 8 * MAX_NT) continue;
       const int key0 = it.seg * SEG;
       it.seq = t.seq;
       it.row0 = t.row0;
@@ -1385,7 +1392,7 @@ __global__ void __launch_bounds__(256) attn_fold_kernel(const __grid_constant__ 
   const int i = inv::warp_upper(a.rb.n_seqs, r, lane, [&](int j) { return a.rb.q_start[j]; });
   if (i < 0) return;
   Tile t;
-  if (!load_seq(a, i, lane, t) || r >= t.row0 + t.n_new) return;
+  if (!load_seq(a, i, lane, t) || r < t.row0 || r >= t.row0 + t.n_new) return;
   if (a.by_seq && t.n_new > a.few) return;  // its rows are finished already
   const int n = t.len - t.n_new + (r - t.row0) + 1, S = (n + SEG - 1) / SEG;
   const int64_t rs = part_index(a, i, r - t.row0, r, (int)(wid - (int64_t)r * a.Hq));

@@ -9,7 +9,7 @@ using inv::record_status;
 constexpr int kAppendThreads = 256;
 
 // HBM bound (a row reads 512 bytes a head, writes 512 a query and 260 a key or
-// value head).  One CTA per row, one warp per head (warp w takes heads w, w + 8,
+// value head).  One CTA per row (and one that checks q_start), one warp per head (warp w takes heads w, w + 8,
 // ...).  Lane l holds the dims 2l, 2l+1, 64+2l, 65+2l, so a rotary pair (i, i+64) is
 // in one lane and a warp's loads are two contiguous 256-byte runs.  A warp requests
 // kBatch heads before it looks up the row's sequence, position and page (three
@@ -24,7 +24,15 @@ __global__ void __launch_bounds__(kAppendThreads)
                      const float* __restrict__ q_gain, const float* __restrict__ k_gain, double eps,
                      float* __restrict__ q_out, int* status) {
   constexpr int W = kAppendThreads / 32;
-  const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0) {
+    // the rows' CTAs see only their own sequence's part of q_start
+    for (int j = threadIdx.x; j < rb.n_seqs; j += kAppendThreads) {
+      const int q0 = rb.q_start[j], q1 = rb.q_start[j + 1];
+      if (q0 < 0 || q1 < q0 || q1 > T) record_status(status, INV_ERR_INVALID_ARG);
+    }
+    return;
+  }
+  const int r = blockIdx.x - 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hkv = c.n_kv_heads, H = Hq + 2 * Hkv;
   float2 x[kBatch][2];
   const auto request = [&](int h0) {
@@ -41,12 +49,14 @@ __global__ void __launch_bounds__(kAppendThreads)
   request(warp);
   const int i = inv::warp_upper(rb.n_seqs, r, lane, [&](int j) { return rb.q_start[j]; });
   if (i < 0) return;
-  const int q1 = rb.q_start[i + 1];
+  const int q0 = rb.q_start[i], q1 = rb.q_start[i + 1];
   if (r >= q1) return;  // behind the last sequence
   const int len = rb.len[i];
   const int64_t pos = (int64_t)len - (q1 - r);
   int page = -1;
-  if (pos >= 0 && pos < max_pos && len >= q1 - rb.q_start[i] && (pos >> c.page_shift) < rb.ld_table)
+  // (r < q0: q_start descends and the search went astray)
+  if (q0 >= 0 && r >= q0 && q1 <= T && pos >= 0 && pos < max_pos && len >= q1 - q0 &&
+      (pos >> c.page_shift) < rb.ld_table)
     page = rb.page_table[i * rb.ld_table + (pos >> c.page_shift)];
   if (page < 0 || page >= c.n_pages) {
     if (threadIdx.x == 0) record_status(status, INV_ERR_INVALID_ARG);
@@ -139,7 +149,7 @@ int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads, const 
   if ((low & 7u) || !inv::aligned16(qkv) || !inv::aligned16(cache->k) || !inv::aligned16(cache->v))
     return INV_ERR_INVALID_ARG;
   const inv::RaggedBatch rb = {page_table, ld_table, n_seqs, q_start, len};
-  kv_append_kernel<<<(unsigned)T, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+  kv_append_kernel<<<(unsigned)T + 1u, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       qkv, ld_qkv, T, n_heads, inv::paged_view(*cache), rb, rope_cos, rope_sin, max_pos, q_gain, k_gain, eps, q_out,
       inv::status_ptr());
   INV_CHECK_LAUNCH();

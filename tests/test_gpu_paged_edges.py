@@ -1,0 +1,103 @@
+"""Calls of the paged-cache operators at the edges of what their documentation
+allows: contradicting descriptors, values that are not numbers, workspaces of
+other calls, lengths next to 2^31."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import status
+from test_gpu_paged import SCALE, batch, check_attend, gen, i32, inv, pool, tables  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------- descriptors ---
+
+Q_START = [  # q_start of 3 sequences over 6 rows, the sequences it contradicts, rows that are still right
+    ([0, 2, 4, 7], [2], [0, 1, 2, 3]),
+    ([-1, 2, 4, 6], [0], [2, 3, 4, 5]),
+    ([-9, -9, 4, 6], [0, 1], [4, 5]),
+    ([0, 2, 4, 2 ** 31 - 1], [2], [0, 1, 2, 3]),
+    ([-2 ** 31, 2, 4, 6], [0], [2, 3, 4, 5]),
+    ([0, 2, 2, 0], [2], []),
+    ([0, 4, 2, 6], [1], []),
+    ([6, 4, 2, 0], [0, 1, 2], []),
+    ([0, 2, 9, 9], [1, 2], [0, 1]),
+]
+
+
+@pytest.mark.parametrize("q_start,wrong,right", Q_START)
+def test_q_start_that_contradicts_the_call_is_recorded(inv, q_start, wrong, right):  # noqa: F811
+    hq, hkv, page = 4, 2, 16
+    lens, news = [40, 50, 20], [2, 2, 2]
+    n_pages, table, start, ln = batch(lens, news, page, seed=71)
+    cache = pool(inv, n_pages, hkv, page, seed=72)
+    q = torch.randn(6, hq, 128, generator=gen(73), device="cuda")
+    want = inv.attn_paged(q, cache, table, start, ln, SCALE)
+    assert status() == inv.INV_OK
+    bad = i32(q_start)
+    for mq in (None, 2):
+        out = torch.full_like(q, 5.0)
+        inv.attn_paged(q, cache, table, bad, ln, SCALE, max_q_bound=mq, out=out)
+        assert status() == inv.INV_ERR_INVALID_ARG
+        assert torch.equal(out[right], want[right])
+        if right:  # nothing overlaps: the other rows are of no sound sequence
+            rest = [r for r in range(6) if r not in right]
+            assert (out[rest] == 5.0).all()
+    # append: the same rows, and nothing but these rows' places in the cache
+    x = torch.randn(6, (hq + 2 * hkv) * 128, generator=gen(74), device="cuda")
+    cos, sin = tables(inv, 64)
+    old = cache.k.clone(), cache.v.clone()
+    good_q = inv.kv_append_paged(x, cache, table, start, ln, cos, sin)
+    good = cache.k.clone(), cache.v.clone()
+    assert status() == inv.INV_OK
+    cache.k.copy_(old[0]), cache.v.copy_(old[1])
+    qo = torch.full_like(q, 5.0)
+    inv.kv_append_paged(x, cache, table, bad, ln, cos, sin, q_out=qo)
+    assert status() == inv.INV_ERR_INVALID_ARG
+    assert torch.equal(qo[right], good_q[right])
+    if right:
+        rest = [r for r in range(6) if r not in right]
+        assert (qo[rest] == 5.0).all()
+    written = torch.zeros(n_pages, page, dtype=torch.bool, device="cuda")
+    may = torch.zeros_like(written)
+    for i in range(3):
+        for t in range(max(0, lens[i] - 6), lens[i]):
+            may[int(table[i, t // page]), t % page] = True
+    for r in right:
+        i, t = r // 2, lens[r // 2] - 2 + r % 2
+        written[int(table[i, t // page]), t % page] = True
+    for now, was, full in zip((cache.k, cache.v), old, good):
+        now, was, full = now.transpose(1, 2), was.transpose(1, 2), full.transpose(1, 2)
+        keep = ~(written if right else may)  # rows of overlapping sequences may land at any of their last places
+        assert torch.equal(now[keep], was[keep]) and torch.equal(now[written], full[written])
+
+
+def test_q_start_that_descends_in_a_long_batch(inv):  # noqa: F811
+    """Tiles and partial results of sequences whose rows overlap, beside sound ones; more sequences than rows."""
+    hq, hkv, page = 8, 2, 32
+    q = torch.randn(300, hq, 128, generator=gen(75), device="cuda")
+    lens = [700, 650, 400, 300]
+    n_pages, table, _, ln = batch(lens, [1] * 4, page, seed=76)
+    cache = pool(inv, n_pages, hkv, page, seed=77)
+    for st in ([0, 300, 100, 200, 300], [300, 0, 300, 0, 300], [0, 100, 300, 10, 20], [250, 10, 5, 260, 40]):
+        wide = torch.full((900, hq, 128), 5.0, device="cuda")
+        inv.attn_paged(q, cache, table, i32(st), ln, SCALE, out=wide[300:600])
+        assert status() == inv.INV_ERR_INVALID_ARG
+        assert (wide[:300] == 5.0).all() and (wide[600:] == 5.0).all()
+    # 40 sequences over 3 rows: what is wrong stands behind the row count
+    n = 40
+    table1 = table[:1].expand(n, -1).contiguous()
+    st = [0, 3] + [3] * (n - 1)
+    x = torch.randn(3, (hq + 2 * hkv) * 128, generator=gen(78), device="cuda")
+    cos, sin = tables(inv, 1024)
+    ln1 = i32([700] * n)
+    inv.kv_append_paged(x, cache, table1, i32(st), ln1, cos, sin)
+    assert status() == inv.INV_OK
+    st[30] = 2
+    inv.kv_append_paged(x, cache, table1, i32(st), ln1, cos, sin)
+    assert status() == inv.INV_ERR_INVALID_ARG
+    inv.attn_paged(q[:3], cache, table1, i32(st), ln1, SCALE)
+    assert status() == inv.INV_ERR_INVALID_ARG
