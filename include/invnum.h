@@ -527,10 +527,11 @@ INV_API int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const i
                        uint16_t* out_hi, uint16_t* out_lo, void* workspace, size_t ws_bytes, inv_stream stream);
 
 /* ------------------------------------------------------------------------
- * softmax_rows -- probs[r][j] = exp(t_j - max t) / sum exp(t_j - max t) with
- * t_j = logits[r][j] * inv_temperature, in fp32, one fixed reduction order per
- * n (batch-invariant).  -inf logits get probability 0; a row of nothing but
- * -inf gets zeros.  probs may be logits (same pointer and ld).
+ * softmax_rows -- probs[r][j] = exp(t_j) / sum exp(t_j) with t_j =
+ * (logits[r][j] - max_j logits[r][j]) * inv_temperature, in fp32, one fixed
+ * reduction order per n (batch-invariant).  -inf logits get probability 0; a
+ * row of nothing but -inf gets zeros.  A row that holds a NaN or +inf is NaN
+ * throughout.  probs may be logits (same pointer and ld).
  *   logits : fp32 [rows][ld], probs : fp32 [rows][ld_p], the first n used.
  *   inv_temperature : finite, > 0.
  * Errors: INV_ERR_INVALID_ARG.

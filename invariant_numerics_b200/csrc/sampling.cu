@@ -32,6 +32,13 @@ __device__ __forceinline__ void store_cluster(void* p, uint32_t r, uint64_t v) {
 
 constexpr int kMaxCluster = 8;
 
+// The larger value; NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Elements i .. i+3 of a row of n; kVec: 16-byte aligned.
 template <bool kVec>
 __device__ __forceinline__ float4 load4(const float* p, int i, int n, float none) {
@@ -48,7 +55,8 @@ __device__ __forceinline__ float4 load4(const float* p, int i, int n, float none
 // HBM bound: 8 bytes an element.  Part c of a row (32 THR elements; thread t owns
 // every THR-th one from t on: coalesced for any row stride): m_c, s_c = sum exp((x -
 // m_c) t); the row: M = max m_c, S = sum_c s_c exp((m_c - M) t) in ascending c; y =
-// exp((x - m_c) t) (exp((m_c - M) t) / S).  THR and the number of parts follow from n
+// exp((x - m_c) t) (exp((m_c - M) t) / S).  The maxima keep NaN, so a row with one is
+// NaN throughout, wherever it stands.  THR and the number of parts follow from n
 // alone, so the order of the sum does too.  21 us for 320 rows of 32000 (3.9 TB/s of
 // data that partly stays in L2; one CTA a row that read it again for the sum took 44 us),
 // 5 us for 3 rows of 32003: launch, cluster barrier and two trips to memory.
@@ -58,12 +66,12 @@ template <int THR>
 __device__ __forceinline__ float block_max(float m, float* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[warp] = m;
   __syncthreads();
   m = red[lane & (THR / 32 - 1)];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 template <int THR>
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(THR, THR == 256 ? 5 : 1024 / THR)
 #pragma unroll
   for (int j = 0; j < kSoftVals; ++j) v[j] = j * THR < left ? xr[j * THR] : -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kSoftVals; ++j) m = fmaxf(m, v[j]);
+  for (int j = 0; j < kSoftVals; ++j) m = max_nan(m, v[j]);
   m = block_max<THR>(m, red_m);
   const bool none = m == -INFINITY;  // nothing but -inf in this part
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -115,12 +123,13 @@ __global__ void __launch_bounds__(THR, THR == 256 ? 5 : 1024 / THR)
   cluster_arrive();
   cluster_wait();
   float M = -INFINITY, S = 0.0f;
-  for (uint32_t q = 0; q < parts_n; ++q) M = fmaxf(M, __uint_as_float((uint32_t)parts[q]));
+  for (uint32_t q = 0; q < parts_n; ++q) M = max_nan(M, __uint_as_float((uint32_t)parts[q]));
   for (uint32_t q = 0; q < parts_n; ++q) {
     const float mq = __uint_as_float((uint32_t)parts[q]), sq = __uint_as_float((uint32_t)(parts[q] >> 32));
     if (mq != -INFINITY) S = __fadd_rn(S, __fmul_rn(sq, expf(__fmul_rn(__fsub_rn(mq, M), it))));
   }
-  const float f = none ? 0.0f : __fmul_rn(expf(__fmul_rn(__fsub_rn(m, M), it)), __frcp_rn(S));
+  // (a part without weight in a row with NaN: 0 NaN)
+  const float f = M == -INFINITY ? 0.0f : __fmul_rn(expf(__fmul_rn(__fsub_rn(m, M), it)), __frcp_rn(S));
   float* yr = y + r * ld_y + first;
 #pragma unroll
   for (int j = 0; j < kSoftVals; ++j)
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(kLongThreads)
   const float* xr = x + r * ld;
   float* yr = y + r * ld_y;
   float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kLongThreads) m = fmaxf(m, xr[i]);
+  for (int i = threadIdx.x; i < n; i += kLongThreads) m = max_nan(m, xr[i]);
   m = block_max<kLongThreads>(m, red_m);
   const bool none = m == -INFINITY;
   float s = 0.0f;

@@ -101,3 +101,44 @@ def test_q_start_that_descends_in_a_long_batch(inv):  # noqa: F811
     assert status() == inv.INV_ERR_INVALID_ARG
     inv.attn_paged(q[:3], cache, table1, i32(st), ln1, SCALE)
     assert status() == inv.INV_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ softmax ---
+
+@pytest.mark.parametrize("n", [1, 5, 1000, 8192, 8193, 16385, 65536, 65537, 131073, 262144, 262145, 300001])
+def test_softmax_rows_with_nan_and_infinity(inv, n):  # noqa: F811
+    """NaN or +inf anywhere makes the row NaN, as the formula does; rows without are as in a call of their own."""
+    part = 32 * (256 if n <= 65536 else 512 if n <= 131072 else 1024)  # elements of a CTA
+    base = torch.randn(n, generator=gen(n), device="cuda") * 4
+    base[::7] = -math.inf
+    base[n // 2] = 1.5
+    places = sorted({0, 1, n // 3, n - 1, min(part, n) - 1, min(part, n - 1)} & set(range(n)))
+    rows, is_nan = [base], [False]
+    for bad in (math.nan, -math.nan, math.inf):
+        for at in places:
+            x = base.clone()
+            x[at] = bad
+            rows.append(x), is_nan.append(True)
+            y = torch.full_like(base, -math.inf)  # nothing finite beside it
+            y[at] = bad
+            rows.append(y), is_nan.append(True)
+    nothing = torch.full_like(base, -math.inf)
+    rows += [nothing * -1, torch.full_like(base, math.nan), nothing]
+    is_nan += [True, True, False]
+    for a in range(0, n, part):  # one part of nothing but NaN
+        x = base.clone()
+        x[a:a + part] = math.nan
+        rows.append(x), is_nan.append(True)
+    x = torch.stack(rows)
+    y = inv.softmax_rows(x, 0.9)
+    is_nan = torch.tensor(is_nan, device="cuda")
+    assert torch.isnan(y[is_nan]).all() and not torch.isnan(y[~is_nan]).any()
+    # the formula's NaN rows (torch has NaN for a row of nothing but -inf too)
+    lowest = (x == -math.inf).all(1)
+    assert torch.equal(torch.isnan(torch.softmax(x.double(), -1)).all(1), is_nan | lowest)
+    assert int((lowest & ~is_nan).sum()) == 1 and (y[lowest] == 0).all()
+    # two exponents of at most 40 (two roundings each), exp, the factor and n / 4096 + 32 additions: 290 2^-24
+    want = torch.softmax(base.double() * float(np.float32(0.9)), -1)
+    assert ((y[0].double() - want).abs() <= 290 * 2.0 ** -24 * want + 1e-38).all()
+    assert torch.equal(inv.softmax_rows(x[:1].contiguous(), 0.9), y[:1])
+    assert status() == inv.INV_OK
