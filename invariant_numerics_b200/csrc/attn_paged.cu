@@ -1012,9 +1012,10 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
         m = fmaxf(m, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
       }
       sm.red[0][hf][r].x = m;
-      asm volatile("bar.sync 1, %0;" ::"n"(SOFT_T) : "memory");
+      asm volatile("barrier.cta.sync 1, %0;" ::"n"(SOFT_T) : "memory");
       m = fmaxf(m, sm.red[0][hf ^ 1][r].x);
-      asm volatile("bar.sync 1, %0;" ::"n"(SOFT_T) : "memory");
+      asm volatile("barrier.cta.sync 1, %0;" ::"n"(SOFT_T) : "memory");
+      __syncwarp();  // the tensor memory accesses below are the whole warp's, as all of them
       const int e = inv::norm_exp(m);
       const float f = inv::pow2f(e);
       kap = __fmul_rn(a.sigma_l2, inv::pow2f(1 - e));
@@ -1104,6 +1105,7 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
 #pragma unroll
           for (int j = 0; j < 4; ++j) L[j] = __fmul_rn(L[j], alpha);
         }
+        __syncwarp();
         float2 g = make_float2(0.0f, 0.0f);
         if (full) {
 #pragma unroll 1

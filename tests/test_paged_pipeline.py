@@ -12,8 +12,8 @@ import re
 
 import pytest
 
-SRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "invariant_numerics_b200", "csrc",
-                   "attn_paged.cu")
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "invariant_numerics_b200", "csrc")
+SRC = os.path.join(CSRC, "attn_paged.cu")
 SCALE_RING = 4  # blocks of scales held
 
 
@@ -160,3 +160,13 @@ def test_the_model_sees_a_missing_wait():
     assert unordered(40, 8, 2) == [] and unordered(40, 16, 3) == []
     with pytest.raises(AssertionError, match="wait for one another"):
         clocks({"a": [("wait", ("x",), 0), ("arrive", ("y",), 0)], "b": [("wait", ("y",), 0), ("arrive", ("x",), 0)]})
+
+
+@pytest.mark.parametrize("name", ["attn_paged.cu", "kv_append.cu", "sampling.cu"])
+def test_barriers_do_not_count_on_converged_warps(name):
+    """Barriers stand behind branches on the lane; in PTX's aligned forms (`bar` is one) a warp's threads must come
+    together, which such a branch does not promise."""
+    asm = " ".join(re.findall(r'"((?:[^"\\]|\\.)*)"', open(os.path.join(CSRC, name)).read()))
+    barriers = re.findall(r"\b(?:bar|barrier)\.[\w.:]+", asm)
+    assert [b for b in barriers if ".aligned" in b or b.startswith("bar.")] == []
+    assert barriers or name == "kv_append.cu"
