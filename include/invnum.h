@@ -445,8 +445,8 @@ INV_API int prefill_layer(const inv_layer_config* cfg, const inv_layer_weights* 
  * A sequence whose q_start entries lie outside 0 .. T or descend, one whose len
  * is smaller than its number of new tokens or beyond the call's bounds, and a
  * page number outside the cache, record INV_ERR_INVALID_ARG; the rows concerned
- * are skipped (attn_paged: a row that reaches a bad page gets unspecified finite
- * values).  Where q_start descends, which sequence a row belongs to is not
+ * are skipped (attn_paged: the keys and values of a bad page count as zeros).
+ * Where q_start descends, which sequence a row belongs to is not
  * defined: any row of the call may be skipped or get unspecified values.
  * ------------------------------------------------------------------------ */
 typedef struct {

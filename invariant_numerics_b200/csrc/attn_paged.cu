@@ -337,26 +337,32 @@ __global__ void __launch_bounds__(TH, 2)
       it.pos0 = t.len - t.n_new;
       it.n_keys = min(SEG, t.len - key0);
       if (it.n_keys <= 0) continue;
-      // lane j: page j of the segment (at most 32), as the cache row of this head's first key
+      // lane j: page j of the segment (at most 32), as the cache row of this head's first key; -1: none, or a page
+      // outside the cache, whose keys and values count as zero (scales 0, whatever codes lie in the slot)
       const int npg = (it.n_keys + ps - 1) >> sh;
-      int row = 0;
+      int row = -1;
       if (lane < npg) {
-        int pg = a.rb.page_table[t.seq * a.rb.ld_table + (key0 >> sh) + lane];
-        if (pg < 0 || pg >= a.c.n_pages) {
+        const int pg = a.rb.page_table[t.seq * a.rb.ld_table + (key0 >> sh) + lane];
+        if (pg < 0 || pg >= a.c.n_pages)
           record_status(a.status, INV_ERR_INVALID_ARG);
-          pg = 0;
-        }
-        row = (pg * Hkv + it.h) << sh;
+        else
+          row = (pg * Hkv + it.h) << sh;
       }
+      const unsigned pages = __ballot_sync(0xffffffffu, row >= 0);
       const int ab = n_item & 1;
       if (n_item >= 2) ok = bar_wait<true>(&sm.item_empty[ab], ((n_item >> 1) - 1) & 1, a, &sm.abort) && ok;
       if (!ok) break;
-      if (lane == 0) {
-        sm.item[ab] = it;
-        inv::mbar_arrive_expect_tx(&sm.item_full[ab], npg * ps * 8);
+      if (lane < npg && row < 0) {
+        for (int j = 0; j < ps; ++j) sm.ks[ab][(lane << sh) + j] = sm.vs[ab][(lane << sh) + j] = 0.0f;
+        inv::fence_proxy_async_smem();  // before a later item's copies to the same place
       }
       __syncwarp();
-      if (lane < npg && INV_SPAN_IN_BOUNDS(a.status, row, row + ps - 1, ((int64_t)a.c.n_pages * Hkv) << sh)) {
+      if (lane == 0) {
+        sm.item[ab] = it;
+        inv::mbar_arrive_expect_tx(&sm.item_full[ab], __popc(pages) * ps * 8);
+      }
+      __syncwarp();
+      if (row >= 0 && INV_SPAN_IN_BOUNDS(a.status, row, row + ps - 1, ((int64_t)a.c.n_pages * Hkv) << sh)) {
         inv::bulk_load(sm.ks[ab] + (lane << sh), a.c.k_scale + row, ps * 4, &sm.item_full[ab]);
         inv::bulk_load(sm.vs[ab] + (lane << sh), a.c.v_scale + row, ps * 4, &sm.item_full[ab]);
       }
@@ -368,12 +374,14 @@ __global__ void __launch_bounds__(TH, 2)
         if (n_slot >= NST) ok = bar_wait<true>(&sm.empty[s], (n_slot / NST - 1) & 1, a, &sm.abort) && ok;
         if (!ok) break;
         const int kb = (op >> 1) * BLK, nb = (min(BLK, it.n_keys - kb) + box - 1) / box;
-        if (lane == 0) inv::mbar_arrive_expect_tx(&sm.full[s], nb * box * D * 2);
-        __syncwarp();
         // lane j: box j (keys kb + j box ..): both halves of d
         const int kk = kb + lane * box;
         const int r0 = __shfl_sync(0xffffffffu, row, (kk >> sh) & 31);
-        if (lane < nb) {
+        const bool in = lane < nb && r0 >= 0;
+        const unsigned boxes = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) inv::mbar_arrive_expect_tx(&sm.full[s], __popc(boxes) * box * D * 2);
+        __syncwarp();
+        if (in) {
           const CUtensorMap* tm = (op & 1) ? &tm_v : &tm_k;
           uint8_t* dst = sm.ring + s * SLOT + lane * box * 128;
           inv::tma_load_2d(dst, tm, &sm.full[s], 0, r0 + (kk & (ps - 1)));

@@ -103,6 +103,33 @@ def test_q_start_that_descends_in_a_long_batch(inv):  # noqa: F811
     assert status() == inv.INV_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("hq,hkv,page,lens,news", [(8, 2, 16, [300, 700], [1, 3]), (4, 2, 64, [640, 90], [8, 1]),
+                                                   (8, 2, 256, [1100, 300], [2, 1]), (8, 2, 32, [900, 200], [300, 40]),
+                                                   (32, 8, 64, [1300, 700], [1290, 2])])
+def test_a_bad_page_counts_as_zeros(inv, hq, hkv, page, lens, news):  # noqa: F811
+    """A page number outside the cache: the bits of a page of zeros in its place, whatever page 0 holds."""
+    n_pages, table, start, ln = batch(lens, news, page, seed=81)
+    cache = pool(inv, n_pages + 2, hkv, page, seed=82)
+    cache.k_scale[0], cache.v_scale[0] = math.nan, math.inf  # of no sequence
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        t[n_pages + 1] = 0
+    table = torch.where(table >= 0, table + 1, table)
+    q = torch.randn(sum(news), hq, 128, generator=gen(83), device="cuda")
+    for bad, spots in ((-1, [(0, 0)]), (n_pages + 2, [(0, 1), (1, 0)]), (2 ** 31 - 1, [(0, lens[0] // page // 2)]),
+                       (-2 ** 31, [(0, (lens[0] - 1) // page), (1, (lens[1] - 1) // page)]),
+                       (-7, [(1, j) for j in range(-(-lens[1] // page))])):
+        wrong, zeros = table.clone(), table.clone()
+        for i, j in spots:
+            wrong[i, j], zeros[i, j] = bad, n_pages + 1
+        want = inv.attn_paged(q, cache, zeros, start, ln, SCALE)
+        assert status() == inv.INV_OK and torch.isfinite(want).all()
+        got = inv.attn_paged(q, cache, wrong, start, ln, SCALE)
+        assert status() == inv.INV_ERR_INVALID_ARG
+        assert torch.equal(got, want)
+        if bad == -7:  # all pages of sequence 1
+            assert (got[int(start[1]):] == 0).all()
+
+
 # ------------------------------------------------------------------ softmax ---
 
 @pytest.mark.parametrize("n", [1, 5, 1000, 8192, 8193, 16385, 65536, 65537, 131073, 262144, 262145, 300001])
