@@ -508,9 +508,20 @@ INV_API int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads
  *   max_len_bound : host upper bound on every len[i] (<= 0: ld_table *
  *              page_size).  The bounds size the launch and the workspace only.
  *   softmax_scale : sigma >= 0, finite.
- *   workspace: >= attn_paged_workspace_size(...) bytes for the resolved bounds,
- *              16-byte aligned (may be NULL if that is 0).  Calls that overlap
- *              on the GPU need separate workspaces.
+ *   workspace: attn_paged_workspace_size(...) bytes for the resolved bounds (on
+ *              the device of the call: the size depends on its number of SMs),
+ *              16-byte aligned (may be NULL if that is 0).  These let every call
+ *              of no more tokens, sequences and bounds through, although calls
+ *              of fewer tokens may ask for more: a few long sequences are split
+ *              over their keys, with partial results per row and segment of 512
+ *              keys, where many tokens are not.  A split whose results do not
+ *              fit the workspace is left out (same bits; 8192 keys, 32 / 8
+ *              heads: 64 tokens take 339 us against 79, 512 tokens 333 against
+ *              417).  The least that a call takes, else INV_ERR_WORKSPACE:
+ *              min(T, n_seqs * (32 n_kv_heads / n_heads)) * n_heads *
+ *              ceil(max_len_bound / 512) * 520 bytes, or 0 if that is one
+ *              segment and max_q_bound * n_heads / n_kv_heads <= 32.  Calls that
+ *              overlap on the GPU need separate workspaces.
  * Errors: INV_ERR_INVALID_ARG; INV_ERR_UNSUPPORTED_SHAPE unless head_dim == 128,
  * page_size as above, n_heads / n_kv_heads is an integer from 1 to 16 and
  * n_kv_heads <= 65535;

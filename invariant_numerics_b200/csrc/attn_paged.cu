@@ -48,6 +48,7 @@ struct AttnArgs {
   inv::RaggedBatch rb;
   int max_q, max_len, S_max;
   int few;          // sequences with at most this many new tokens are the mma.sync kernel's
+  int direct;       // rows of the tcgen05 kernel are finished there and have no partials
   int by_seq;       // partials indexed by (sequence, token < few) instead of by row
   int segs;         // segments per CTA of the tcgen05 kernel (split over keys)
   float sigma_l2;   // sigma log2 e
@@ -1403,7 +1404,7 @@ __global__ void __launch_bounds__(256) attn_fold_kernel(const __grid_constant__ 
   if (i < 0) return;
   Tile t;
   if (!load_seq(a, i, lane, t) || r < t.row0 || r >= t.row0 + t.n_new) return;
-  if (a.by_seq && t.n_new > a.few) return;  // its rows are finished already
+  if (a.direct && t.n_new > a.few) return;  // its rows are finished already
   const int n = t.len - t.n_new + (r - t.row0) + 1, S = (n + SEG - 1) / SEG;
   const int64_t rs = part_index(a, i, r - t.row0, r, (int)(wid - (int64_t)r * a.Hq));
   if (!INV_SPAN_IN_BOUNDS(a.status, rs, rs + S - 1, part_count(a))) return;
@@ -1441,6 +1442,7 @@ int allow_smem(F kernel, size_t bytes, bool (&done)[64]) {
 }
 
 constexpr int MAX_GRID_YZ = 65535;
+constexpr size_t PART_BYTES = D * sizeof(float) + sizeof(float2);  // of one segment's result
 
 int segments(int max_len) { return max_len / SEG + (max_len % SEG != 0); }
 
@@ -1450,30 +1452,35 @@ int segments(int max_len) { return max_len / SEG + (max_len % SEG != 0); }
 int few_tokens(int G) { return 8 * MAX_NT / G; }
 int64_t many_tiles(int T, int n_seqs, int G) { return (int64_t)T / (MANY_ROWS / G) + n_seqs; }
 
-// How a call's work is cut: by its sizes and bounds only, and without any
-// effect on the bits.
+// How a call's work is cut: by its sizes and bounds, the GPU's number of SMs and the
+// partial results that the workspace can hold, and without any effect on the bits.
 struct Plan {
   bool many;       // some sequence may have more than few_tokens new tokens
   bool direct;     // a CTA of the tcgen05 kernel takes all segments of its tile and folds them
-  int segs;        // else: segments per CTA
+  bool by_seq;     // partial results by (sequence, token) instead of by row: there are fewer of these
+  int segs;        // segments per CTA, unless direct
   int64_t parts;   // (row, head) pairs with partial results
 };
-Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len) {
+Plan make_plan(int T, int n_seqs, int Hq, int Hkv, int max_q, int max_len, int64_t room) {
   const int G = Hq / Hkv, S = segments(max_len), few = few_tokens(G);
-  Plan p = {max_q > few, false, 1, (int64_t)T * Hq};
+  // rows of sequences with few tokens: these always need their partial results, unless one segment is all there is
+  const int64_t few_rows = std::min<int64_t>(T, (int64_t)n_seqs * few);
+  Plan p = {max_q > few, false, few_rows < T, 1, few_rows * Hq};
   if (!p.many) {
     if (S == 1) p.parts = 0;
     return p;
   }
-  // Direct from two CTAs a SM on: each reads its rows' q once and writes no partial results.
+  // Direct from two CTAs a SM on: each reads its rows' q once and writes no partial results.  Also where the split's
+  // results do not fit the workspace: a workspace for many tokens, which are direct, serves calls of fewer.
   const int sms = inv::sm_count();
   const int64_t tiles = (int64_t)T / (MANY_ROWS / G);
-  p.direct = (tiles + 1) * Hkv >= 2 * sms || S == 1;
+  p.direct = (tiles + 1) * Hkv >= 2 * sms || S == 1 || (int64_t)T * Hq > room;
   if (p.direct) {
     p.segs = S;
-    p.parts = (int64_t)n_seqs * few * Hq;
     return p;
   }
+  p.by_seq = false;
+  p.parts = (int64_t)T * Hq;
   // Split over keys.  In units of one block of 128 keys (4 us) a CTA costs 2 to start and to finish and 4 per
   // segment; n CTAs that do not all fit at once take their sum over the SMs and half a CTA's time at the end.
   // Measured at 32 query and 8 kv heads, 1 / 2 / 4 segments per CTA: 64 tokens over 8192 keys 81 / 72 / 106 us, 512
@@ -1546,8 +1553,8 @@ size_t attn_paged_workspace_size(int T, int n_seqs, int n_heads, int n_kv_heads,
   if (T <= 0 || n_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || max_len_bound <= 0) return 0;
   if (n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 16) return 0;
   const Plan p = make_plan(T, n_seqs, n_heads, n_kv_heads, max_q_bound > 0 && max_q_bound < T ? max_q_bound : T,
-                           max_len_bound);
-  return (size_t)p.parts * segments(max_len_bound) * (D * sizeof(float) + sizeof(float2));
+                           max_len_bound, INT64_MAX);
+  return (size_t)p.parts * segments(max_len_bound) * PART_BYTES;
 }
 
 int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged_kv_cache* cache,
@@ -1574,9 +1581,10 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   a.max_len = max_len_bound > 0 && max_len_bound < room ? max_len_bound : (int)room;
   a.max_q = max_q_bound > 0 && max_q_bound < T ? max_q_bound : T;
   a.S_max = segments(a.max_len);
-  const size_t need = attn_paged_workspace_size(T, n_seqs, n_heads, cache->n_kv_heads, a.max_q, a.max_len);
-  if (ws_bytes < need) return INV_ERR_WORKSPACE;
-  if (need > 0 && !workspace) return INV_ERR_INVALID_ARG;
+  const Plan p = make_plan(T, n_seqs, n_heads, cache->n_kv_heads, a.max_q, a.max_len,
+                           (int64_t)std::min<uint64_t>(ws_bytes / (PART_BYTES * a.S_max), INT64_MAX));
+  if (ws_bytes / (PART_BYTES * a.S_max) < (uint64_t)p.parts) return INV_ERR_WORKSPACE;
+  if (p.parts > 0 && !workspace) return INV_ERR_INVALID_ARG;
   a.q = q;
   a.ld_q = ld_q;
   a.T = T;
@@ -1586,10 +1594,10 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
   a.rb = {page_table, ld_table, n_seqs, q_start, len};
   a.sigma_l2 = (float)((double)softmax_scale * 1.4426950408889634);
   a.part_o = static_cast<float*>(workspace);
-  const Plan p = make_plan(T, n_seqs, n_heads, cache->n_kv_heads, a.max_q, a.max_len);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.parts * a.S_max * D);
   a.few = few_tokens(G);
-  a.by_seq = p.many && p.direct;
+  a.direct = p.direct;
+  a.by_seq = p.by_seq;
   a.segs = p.segs;
   if ((int64_t)n_seqs * a.S_max > 0x7fffffff || many_tiles(T, n_seqs, G) > 0x7fffffff) return INV_ERR_UNSUPPORTED_SHAPE;
   a.out = out;

@@ -484,7 +484,8 @@ def attn_paged_workspace_size(T: int, n_seqs: int, n_heads: int, n_kv_heads: int
 def attn_paged(q, cache: PagedKVCache, page_table, q_start, lens, softmax_scale, max_q_bound=None, max_len_bound=None,
                out=None, want_split=False, workspace=None, stream=None):
     """Causal attention of a ragged batch's new tokens over their pages: q fp32 [T, Hq, 128] -> out fp32 [T, Hq, 128]
-    (and hi/lo if want_split).  Without out, the rows of no sequence are unspecified."""
+    (and hi/lo if want_split).  Without out, the rows of no sequence are unspecified.  A workspace of the size for the
+    most tokens, sequences and bounds serves every call of fewer (one of the call's own size may be faster)."""
     dev = _home(q)
     n = _ragged(cache, page_table, q_start, lens, dev)
     _expect(q, torch.float32, dev, "q", contiguous=False)

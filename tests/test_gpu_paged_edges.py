@@ -130,6 +130,56 @@ def test_a_bad_page_counts_as_zeros(inv, hq, hkv, page, lens, news):  # noqa: F8
             assert (got[int(start[1]):] == 0).all()
 
 
+# ---------------------------------------------------------------- workspace ---
+
+@pytest.mark.parametrize("hq,hkv,page,most", [(32, 8, 64, 2500), (8, 1, 16, 5000)])
+def test_attn_paged_workspace_of_a_larger_call(inv, hq, hkv, page, most):  # noqa: F811
+    """One workspace, sized for the largest chunk of a prompt, for its chunks down to one token: the same bits as with
+    each call's own, and nothing behind it is written."""
+    n = most + 100
+    n_pages, table, _, ln = batch([n], [1], page, seed=84)
+    cache = pool(inv, n_pages, hkv, page, seed=85)
+    q = torch.randn(most, hq, 128, generator=gen(86), device="cuda")
+    size = inv.attn_paged_workspace_size(most, 1, hq, hkv, most, n)
+    least = min(most, 32 * hkv // hq) * hq * -(-n // 512) * 520
+    assert size >= least and max(inv.attn_paged_workspace_size(t, 1, hq, hkv, t, n) for t in (64, 300, 700)) > size
+    big = torch.full((size + 4096,), 7, dtype=torch.uint8, device="cuda")
+    small = torch.full((least + 4096,), 7, dtype=torch.uint8, device="cuda")
+    for T in (1, 3, 32 * hkv // hq, 32 * hkv // hq + 1, 33, 64, 300, 700, 1100, most):
+        start = i32([0, T])
+        want = inv.attn_paged(q[:T], cache, table, start, ln, SCALE, max_len_bound=n)
+        for ws in (big[:size], small[:least]):
+            got = inv.attn_paged(q[:T], cache, table, start, ln, SCALE, max_len_bound=n, workspace=ws)
+            assert torch.equal(got, want), T
+    assert (big[size:] == 7).all() and (small[least:] == 7).all()
+    # a batch padded far beyond its tokens: partial results by (sequence, token)
+    pad = q[:400]
+    ws = torch.full((least + 4096,), 7, dtype=torch.uint8, device="cuda")
+    got = inv.attn_paged(pad, cache, table, i32([0, 3]), ln, SCALE, max_q_bound=3, max_len_bound=n, workspace=ws[:least])
+    assert torch.equal(got[:3], inv.attn_paged(q[:3], cache, table, i32([0, 3]), ln, SCALE))
+    assert (ws[least:] == 7).all() and status() == inv.INV_OK
+
+
+def test_attn_paged_mixed_batch_in_a_small_workspace(inv):  # noqa: F811
+    """Sequences of few and of many tokens where the split does not fit: few rows have partial results, by row and by
+    sequence, the others none."""
+    hq, hkv, page = 8, 2, 32
+    for lens, news in (([900, 1400, 700, 60], [40, 3, 1, 60]), ([1300, 800], [6, 9]), ([1500, 700, 800], [300, 2, 8])):
+        n_pages, table, start, ln = batch(lens, news, page, seed=87)
+        cache = pool(inv, n_pages, hkv, page, seed=88)
+        T, n = sum(news), max(lens)
+        q = torch.randn(T, hq, 128, generator=gen(89), device="cuda")
+        want = inv.attn_paged(q, cache, table, start, ln, SCALE, max_len_bound=n)
+        least = min(T, 8 * len(lens)) * hq * -(-n // 512) * 520
+        ws = torch.full((least + 4096,), 7, dtype=torch.uint8, device="cuda")
+        got = inv.attn_paged(q, cache, table, start, ln, SCALE, max_len_bound=n, workspace=ws[:least])
+        assert torch.equal(got, want) and (ws[least:] == 7).all()
+        check_attend(inv, q, cache, table, start, ln, got)
+        with pytest.raises(inv.InvError):
+            inv.attn_paged(q, cache, table, start, ln, SCALE, max_len_bound=n, workspace=ws[:least - 16])
+    assert status() == inv.INV_OK
+
+
 # ------------------------------------------------------------------ softmax ---
 
 @pytest.mark.parametrize("n", [1, 5, 1000, 8192, 8193, 16385, 65536, 65537, 131073, 262144, 262145, 300001])

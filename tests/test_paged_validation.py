@@ -128,3 +128,35 @@ def test_the_largest_bounds(inv):
     assert attend(inv, ld_table=1 << 40, nb=0) == WORKSPACE
     assert attend(inv, ld_table=0) == INVALID and attend(inv, ld_table=0, T=0) == OK
     assert attend(inv, hq=70000, ld=70000 * 128, c=cache(inv, hkv=70000)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (16, 1), (8, 8), (24, 8)])
+@pytest.mark.parametrize("n_seqs", [1, 3, 40])
+@pytest.mark.parametrize("bound", [300, 8192, 131072])
+def test_a_workspace_serves_every_smaller_call(inv, hq, hkv, n_seqs, bound):
+    """The size for T tokens lets calls of fewer tokens, sequences and keys through, whatever plan these prefer; and the
+    least that is documented is what a call takes."""
+    size = inv.lib.attn_paged_workspace_size
+    c = cache(inv, hkv=hkv)
+    few, S = 32 * hkv // hq, -(-bound // 512)
+
+    def passes(nb, T, n=n_seqs, mq=0, mlb=bound):
+        # without a pointer: INVALID once the size will do (OK is not reached on a CPU), WORKSPACE before
+        rc = attend(inv, T=T, n=n, hq=hq, ld=hq * 128, c=c, ld_table=1 << 14, mq=mq, mlb=mlb, ws=None, nb=nb)
+        assert rc in (INVALID, WORKSPACE)
+        return rc == INVALID
+
+    tokens = [1, 2, few, few + 1, 2 * few, 33, 64, 100, 300, 512, 700, 1000, 1100, 1152, 2000, 3000, 8192]
+    for T in tokens:
+        mq = T if S == 1 and T * hq <= 32 * hkv else 0
+        if mq:
+            assert size(T, n_seqs, hq, hkv, mq, bound) == 0
+            continue
+        least = min(T, n_seqs * few) * hq * S * 520
+        assert passes(least, T) and not passes(least - 1, T)
+        nb = size(T, n_seqs, hq, hkv, T, bound)
+        assert nb >= least
+        for fewer in tokens:
+            if fewer <= T and not (S == 1 and fewer <= few):
+                assert passes(nb, fewer) and passes(nb, fewer, n=1)
+                assert bound < 1000 or passes(nb, fewer, mlb=bound // 2 + 1)
