@@ -506,7 +506,7 @@ INV_API int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads
  *              (both NULL or both non-NULL).
  *   max_q_bound : host upper bound on the new tokens of a sequence (<= 0: T).
  *   max_len_bound : host upper bound on every len[i] (<= 0: ld_table *
- *              page_size).  The bounds size the launch and the workspace only.
+ *              page_size), at most 2^31 - 512 as a len is.  The bounds size the launch and the workspace only.
  *   softmax_scale : sigma >= 0, finite.
  *   workspace: attn_paged_workspace_size(...) bytes for the resolved bounds (on
  *              the device of the call: the size depends on its number of SMs),

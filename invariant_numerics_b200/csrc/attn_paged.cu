@@ -1444,6 +1444,9 @@ int allow_smem(F kernel, size_t bytes, bool (&done)[64]) {
 constexpr int MAX_GRID_YZ = 65535;
 constexpr size_t PART_BYTES = D * sizeof(float) + sizeof(float2);  // of one segment's result
 
+// The longest sequence: a position rounded up to a whole segment stays below 2^31.
+constexpr int MAX_LEN = 0x7fffffff - (SEG - 1);
+
 int segments(int max_len) { return max_len / SEG + (max_len % SEG != 0); }
 
 // Sequences with at most this many new tokens (32 rows) take the mma.sync kernel: at 32
@@ -1576,7 +1579,7 @@ int attn_paged(const float* q, int64_t ld_q, int T, int n_heads, const inv_paged
       !inv::aligned16(cache->k_scale) || !inv::aligned16(cache->v_scale) || !inv::aligned16(workspace) ||
       ((reinterpret_cast<uintptr_t>(out_hi) | reinterpret_cast<uintptr_t>(out_lo)) & 7u))
     return INV_ERR_INVALID_ARG;
-  const int64_t room = ld_table > 0x7fffffff / cache->page_size ? 0x7fffffff : ld_table * cache->page_size;
+  const int64_t room = ld_table > MAX_LEN / cache->page_size ? MAX_LEN : ld_table * cache->page_size;
   AttnArgs a = {};
   a.max_len = max_len_bound > 0 && max_len_bound < room ? max_len_bound : (int)room;
   a.max_q = max_q_bound > 0 && max_q_bound < T ? max_q_bound : T;

@@ -493,7 +493,7 @@ def attn_paged(q, cache: PagedKVCache, page_table, q_start, lens, softmax_scale,
         raise ValueError("q must be [T, n_heads, 128] with contiguous rows")
     T, Hq, _ = q.shape
     pages = page_table.shape[1]
-    room = pages * cache.page_size
+    room = min(pages * cache.page_size, (1 << 31) - 512)  # the longest sequence a call takes
     mq = T if max_q_bound is None or not 0 < max_q_bound < T else int(max_q_bound)
     mlb = room if max_len_bound is None or not 0 < max_len_bound < room else int(max_len_bound)
     if out is None:

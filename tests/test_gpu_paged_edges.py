@@ -180,6 +180,25 @@ def test_attn_paged_mixed_batch_in_a_small_workspace(inv):  # noqa: F811
     assert status() == inv.INV_OK
 
 
+def test_lengths_next_to_two_to_the_31(inv):  # noqa: F811
+    """A page table of 2^31 positions: short sequences are attended, a length that a segment's end would carry beyond
+    int32 is recorded."""
+    hq = hkv = 1
+    cache = pool(inv, 3, hkv, 256, seed=90)
+    table = torch.zeros(1, 1 << 23, dtype=torch.int32, device="cuda")
+    table[0, 1] = 2
+    q = torch.randn(2, hq, 128, generator=gen(91), device="cuda")
+    want = inv.attn_paged(q[:1], cache, table[:, :4].contiguous(), i32([0, 1]), i32([400]), SCALE)
+    for bound in (None, 400, 2 ** 31, 2 ** 40):
+        got = inv.attn_paged(q[:1], cache, table, i32([0, 1]), i32([400]), SCALE, max_len_bound=bound)
+        assert torch.equal(got, want)
+    assert status() == inv.INV_OK
+    for n in (2 ** 31 - 1, 2 ** 31 - 511):
+        out = torch.full_like(q, 5.0)
+        inv.attn_paged(q[:1], cache, table, i32([0, 1]), i32([n]), SCALE, out=out[:1])
+        assert status() == inv.INV_ERR_INVALID_ARG and (out == 5.0).all()
+
+
 # ------------------------------------------------------------------ softmax ---
 
 @pytest.mark.parametrize("n", [1, 5, 1000, 8192, 8193, 16385, 65536, 65537, 131073, 262144, 262145, 300001])

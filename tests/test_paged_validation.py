@@ -160,3 +160,12 @@ def test_a_workspace_serves_every_smaller_call(inv, hq, hkv, n_seqs, bound):
             if fewer <= T and not (S == 1 and fewer <= few):
                 assert passes(nb, fewer) and passes(nb, fewer, n=1)
                 assert bound < 1000 or passes(nb, fewer, mlb=bound // 2 + 1)
+
+
+def test_the_longest_sequence(inv):
+    """Lengths end at 2^31 - 512, whatever the page table could hold and the bound says: 2^22 - 1 segments."""
+    c = cache(inv, hkv=8)
+    least = 8 * 520 * (2 ** 22 - 1)
+    for ld_table, mlb in ((1 << 40, 0), (1 << 40, 2 ** 31 - 1), (2 ** 27, 0), (2 ** 27, 2 ** 31 - 512)):
+        call = lambda nb: attend(inv, T=1, n=1, hq=8, ld=1024, c=c, ld_table=ld_table, mlb=mlb, ws=None, nb=nb)
+        assert call(least) == INVALID and call(least - 1) == WORKSPACE  # (no pointer: INVALID once the size will do)
