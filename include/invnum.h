@@ -567,7 +567,7 @@ INV_API int softmax_rows(const float* logits, int rows, int n, int64_t ld, float
  *   draft_tokens : int32 [B][max_draft];  u_accept : fp32 [B][max_draft],
  *   u_sample : fp32 [B], in [0, 1).
  *   tokens : int32 [B][max_draft + 1]: x_0 .. x_{k-1}, the next token, then -1.
- *   n_accepted : int32 [B]: k.
+ *   n_accepted : int32 [B]: k.  max_draft : at most 2^30.
  * Errors: INV_ERR_INVALID_ARG.  Device: INV_ERR_INVALID_ARG for a draft token
  * outside [0, vocab) or n_draft outside [0, max_draft]; that sequence gets
  * n_accepted 0 and tokens -1.

@@ -32,6 +32,7 @@ __device__ __forceinline__ void store_cluster(void* p, uint32_t r, uint64_t v) {
 }
 
 constexpr int kMaxCluster = 8;
+constexpr int kMaxDraft = 1 << 30;  // counters a block beyond it stay below 2^31
 
 // The larger value; NaN if either is one.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(THR, THR == 256 ? 5 : 1024 / THR)
     if (j * THR < left) yr[j * THR] = __fmul_rn(v[j], f);
 }
 
-// Rows longer than eight parts: one CTA a row, which reads it three times.
+// Rows longer than eight parts: one CTA a row, which reads it three times (indexes are unsigned: the last step of a
+// row next to 2^31 ends behind it).
 constexpr int kLongThreads = 1024;
 __global__ void __launch_bounds__(kLongThreads)
     softmax_long_kernel(const float* x, int rows, int n, int64_t ld, float it, float* y, int64_t ld_y, int* status) {
@@ -150,17 +152,17 @@ __global__ void __launch_bounds__(kLongThreads)
   const float* xr = x + r * ld;
   float* yr = y + r * ld_y;
   float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kLongThreads) m = max_nan(m, xr[i]);
+  for (unsigned i = threadIdx.x; i < (unsigned)n; i += kLongThreads) m = max_nan(m, xr[i]);
   m = block_max<kLongThreads>(m, red_m);
   const bool none = m == -INFINITY;
   float s = 0.0f;
-  for (int i = threadIdx.x; i < n; i += kLongThreads)
+  for (unsigned i = threadIdx.x; i < (unsigned)n; i += kLongThreads)
     s = __fadd_rn(s, none ? 0.0f : expf(__fmul_rn(__fsub_rn(xr[i], m), it)));
   s = block_sum<kLongThreads>(s, red_s);
   if (threadIdx.x == 0) total = s;
   __syncthreads();
   const float f = none ? 0.0f : __frcp_rn(total);
-  for (int i = threadIdx.x; i < n; i += kLongThreads)
+  for (unsigned i = threadIdx.x; i < (unsigned)n; i += kLongThreads)
     yr[i] = none ? 0.0f : __fmul_rn(expf(__fmul_rn(__fsub_rn(xr[i], m), it)), f);
 }
 
@@ -394,16 +396,17 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_long_kernel(const 
   const float* p = a.target + ((int64_t)b * (D + 1) + k) * a.ld_t;
   const float* q = k < m && a.draft ? a.draft + ((int64_t)b * D + k) * a.ld_d : nullptr;
   const int drop = k < m && !a.draft ? a.draft_tokens[(int64_t)b * D + k] : -1;
-  const int range = ((V + kVerifyWarps - 1) / kVerifyWarps + 31) / 32 * 32;
-  const int j0 = min(V, warp * range), j1 = min(V, j0 + range);
+  // (unsigned: the last warp's range may end behind 2^31)
+  const unsigned range = (((unsigned)V + kVerifyWarps - 1) / kVerifyWarps + 31) / 32 * 32;
+  const unsigned j0 = min((unsigned)V, warp * range), j1 = min((unsigned)V, j0 + range);
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
-    const auto at = [&](int j) {
+    const auto at = [&](unsigned j) {
       if (round) return weight(p[j], 0.0f);
-      return j == drop ? 0.0 : weight(p[j], q ? q[j] : 0.0f);
+      return (int)j == drop ? 0.0 : weight(p[j], q ? q[j] : 0.0f);
     };
     double s = 0.0;
-    for (int j = j0 + lane; j < j1; j += 32) s += at(j);
+    for (unsigned j = j0 + lane; j < j1; j += 32) s += at(j);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) tot[warp] = s;
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_long_kernel(const 
       if (warp != pick) return;
       int last = -1;
       double c0 = before;
-      for (int j = j0; j < j1; j += 32) {
+      for (unsigned j = j0; j < j1; j += 32) {
         const double w = j + lane < j1 ? at(j + lane) : 0.0;
         double c = w;
 #pragma unroll
@@ -437,9 +440,9 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_long_kernel(const 
         }
         const unsigned some = __ballot_sync(0xffffffffu, w > 0.0);
         const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && c0 + c > thr);
-        if (some) last = j + 31 - __clz(some);
+        if (some) last = (int)j + 31 - __clz(some);
         if (hit) {
-          last = j + __ffs(hit) - 1;
+          last = (int)j + __ffs(hit) - 1;
           break;
         }
         c0 += __shfl_sync(0xffffffffu, c, 31);
@@ -509,7 +512,7 @@ int softmax_rows(const float* logits, int rows, int n, int64_t ld, float inv_tem
 int spec_verify(const float* target, int64_t ld_target, const float* draft, int64_t ld_draft, int B, int max_draft,
                 int vocab, const int32_t* draft_tokens, const int32_t* n_draft, const float* u_accept,
                 const float* u_sample, int32_t* tokens, int32_t* n_accepted, inv_stream stream) {
-  if (B < 0 || max_draft < 0 || vocab <= 0 || ld_target < vocab || (draft && ld_draft < vocab))
+  if (B < 0 || max_draft < 0 || max_draft > kMaxDraft || vocab <= 0 || ld_target < vocab || (draft && ld_draft < vocab))
     return INV_ERR_INVALID_ARG;
   if (B == 0) return INV_OK;
   if (!target || !u_sample || !tokens || !n_accepted || (max_draft > 0 && (!draft_tokens || !u_accept)))

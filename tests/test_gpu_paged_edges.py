@@ -238,3 +238,21 @@ def test_softmax_rows_with_nan_and_infinity(inv, n):  # noqa: F811
     assert ((y[0].double() - want).abs() <= 290 * 2.0 ** -24 * want + 1e-38).all()
     assert torch.equal(inv.softmax_rows(x[:1].contiguous(), 0.9), y[:1])
     assert status() == inv.INV_OK
+
+
+def test_the_longest_rows(inv):  # noqa: F811
+    """Rows of 2^31 - 1 elements: the last step of the kernels' loops ends behind them."""
+    n = 2 ** 31 - 1
+    x = torch.full((1, n), -math.inf, device="cuda")
+    at = [0, 2 ** 30 + 5, n - 1025, n - 2, n - 1]
+    x[0, at] = 2.0
+    inv.softmax_rows(x, 1.5, out=x)
+    assert (x[0, at] == float(np.float32(1.0) / np.float32(5.0))).all() and int((x != 0).sum()) == 5
+    none = lambda dtype: torch.empty(1, 0, dtype=dtype, device="cuda")
+    for u, want in ((0.0, 0), (0.3, 2 ** 30 + 5), (0.5, n - 1025), (0.7, n - 2), (0.999, n - 1)):
+        t, a = inv.spec_verify(x.view(1, 1, n), None, none(torch.int32), none(torch.float32),
+                               torch.tensor([u], device="cuda"))
+        assert t.tolist() == [[want]] and a.tolist() == [0]
+    t, a = inv.spec_verify(x.zero_().view(1, 1, n), None, none(torch.int32), none(torch.float32),
+                           torch.tensor([0.5], device="cuda"))
+    assert t.tolist() == [[-1]] and status() == inv.INV_OK

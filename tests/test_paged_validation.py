@@ -169,3 +169,9 @@ def test_the_longest_sequence(inv):
     for ld_table, mlb in ((1 << 40, 0), (1 << 40, 2 ** 31 - 1), (2 ** 27, 0), (2 ** 27, 2 ** 31 - 512)):
         call = lambda nb: attend(inv, T=1, n=1, hq=8, ld=1024, c=c, ld_table=ld_table, mlb=mlb, ws=None, nb=nb)
         assert call(least) == INVALID and call(least - 1) == WORKSPACE  # (no pointer: INVALID once the size will do)
+
+
+def test_verify_refuses_more_drafts_than_its_counters_hold(inv):
+    f = inv.lib.spec_verify
+    for m, want in ((2 ** 31 - 1, INVALID), (2 ** 30 + 1, INVALID), (2 ** 30, OK)):
+        assert f(PTR, 100, None, 0, 0, m, 100, PTR, None, PTR, PTR, PTR, PTR, None) == want
