@@ -140,13 +140,13 @@ __device__ __forceinline__ int64_t part_index(const AttnArgs& a, int seq, int to
 // registers: 276 bytes of spill loads against 208).
 template <bool kRecordRows = false>
 __device__ __forceinline__ bool load_seq(const AttnArgs& a, int i, int lane, Tile& t) {
-  const int q0 = a.rb.q_start[i], q1 = a.rb.q_start[i + 1];
+  const int q0 = inv::start_of(a.rb, i, a.status), q1 = inv::start_of(a.rb, i + 1, a.status);
   if (kRecordRows && lane == 0 && (q0 < 0 || q1 < q0 || q1 > a.T)) record_status(a.status, INV_ERR_INVALID_ARG);
   if (q0 < 0 || q1 <= q0 || q1 > a.T) return false;
   t.seq = i;
   t.row0 = q0;
   t.n_new = q1 - q0;
-  t.len = a.rb.len[i];
+  t.len = inv::len_of(a.rb, i, a.status);
   if (t.n_new > a.max_q || t.len < t.n_new || t.len > a.max_len) {
     if (lane == 0) record_status(a.status, INV_ERR_INVALID_ARG);
     return false;
@@ -159,7 +159,7 @@ __device__ __forceinline__ bool load_seq(const AttnArgs& a, int i, int lane, Til
 // per) >= ceil(n / per)), without a pass over the batch.  False: no such tile (where
 // q_start descends, the search may end at a sequence whose ids begin behind id).
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int id, int per, int lane, Tile& t) {
-  const int i = inv::warp_upper(a.rb.n_seqs, id, lane, [&](int j) { return a.rb.q_start[j] / per + j; });
+  const int i = inv::warp_upper(a.rb.n_seqs, id, lane, [&](int j) { return inv::start_of(a.rb, j, a.status) / per + j; });
   if (i < 0 || !load_seq(a, i, lane, t)) return false;
   const int j = id - (t.row0 / per + i);
   if (j < 0 || j > (t.n_new - 1) / per) return false;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(TH, 2)
       const int npg = (it.n_keys + ps - 1) >> sh;
       int row = -1;
       if (lane < npg) {
-        const int pg = a.rb.page_table[t.seq * a.rb.ld_table + (key0 >> sh) + lane];
+        const int pg = inv::page_of(a.rb, t.seq, (key0 >> sh) + lane, a.status);
         if (pg < 0 || pg >= a.c.n_pages)
           record_status(a.status, INV_ERR_INVALID_ARG);
         else
@@ -924,7 +924,7 @@ __device__ __forceinline__ float2 weights(uint32_t src, const float* ks, const f
 // last key and for a page outside the cache.
 __device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int seq, int h, int key, int last) {
   if (key >= last) return -1;
-  const int sh = a.c.page_shift, pg = a.rb.page_table[seq * a.rb.ld_table + (key >> sh)];
+  const int sh = a.c.page_shift, pg = inv::page_of(a.rb, seq, key >> sh, a.status);
   if (pg < 0 || pg >= a.c.n_pages) {
     record_status(a.status, INV_ERR_INVALID_ARG);
     return -1;
@@ -1279,7 +1279,7 @@ __global__ void __launch_bounds__(MANY_T, 1) attn_many_kernel(const __grid_const
     const auto put_pages = [&](int j) {
       if (lane < BLK / 16) {
         const int key = (b0 + j) * BLK + 16 * lane;
-        int pg = key < last ? a.rb.page_table[t.seq * a.rb.ld_table + (key >> a.c.page_shift)] : -1;
+        int pg = key < last ? inv::page_of(a.rb, t.seq, key >> a.c.page_shift, a.status) : -1;
         if (key < last && (pg < 0 || pg >= a.c.n_pages)) {
           record_status(a.status, INV_ERR_INVALID_ARG);
           pg = -1;
@@ -1400,7 +1400,7 @@ __global__ void __launch_bounds__(256) attn_fold_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31;
   if (wid >= (int64_t)a.T * a.Hq) return;
   const int r = (int)(wid / a.Hq);
-  const int i = inv::warp_upper(a.rb.n_seqs, r, lane, [&](int j) { return a.rb.q_start[j]; });
+  const int i = inv::warp_upper(a.rb.n_seqs, r, lane, [&](int j) { return inv::start_of(a.rb, j, a.status); });
   if (i < 0) return;
   Tile t;
   if (!load_seq(a, i, lane, t) || r < t.row0 || r >= t.row0 + t.n_new) return;

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kAppendThreads)
   if (blockIdx.x == 0) {
     // the rows' CTAs see only their own sequence's part of q_start
     for (int j = threadIdx.x; j < rb.n_seqs; j += kAppendThreads) {
-      const int q0 = rb.q_start[j], q1 = rb.q_start[j + 1];
+      const int q0 = inv::start_of(rb, j, status), q1 = inv::start_of(rb, j + 1, status);
       if (q0 < 0 || q1 < q0 || q1 > T) record_status(status, INV_ERR_INVALID_ARG);
     }
     return;
@@ -47,21 +47,22 @@ __global__ void __launch_bounds__(kAppendThreads)
     }
   };
   request(warp);
-  const int i = inv::warp_upper(rb.n_seqs, r, lane, [&](int j) { return rb.q_start[j]; });
+  const int i = inv::warp_upper(rb.n_seqs, r, lane, [&](int j) { return inv::start_of(rb, j, status); });
   if (i < 0) return;
-  const int q0 = rb.q_start[i], q1 = rb.q_start[i + 1];
+  const int q0 = inv::start_of(rb, i, status), q1 = inv::start_of(rb, i + 1, status);
   if (r >= q1) return;  // behind the last sequence
-  const int len = rb.len[i];
+  const int len = inv::len_of(rb, i, status);
   const int64_t pos = (int64_t)len - (q1 - r);
   int page = -1;
   // (r < q0: q_start descends and the search went astray)
   if (q0 >= 0 && r >= q0 && q1 <= T && pos >= 0 && pos < max_pos && len >= q1 - q0 &&
       (pos >> c.page_shift) < rb.ld_table)
-    page = rb.page_table[i * rb.ld_table + (pos >> c.page_shift)];
+    page = inv::page_of(rb, i, pos >> c.page_shift, status);
   if (page < 0 || page >= c.n_pages) {
     if (threadIdx.x == 0) record_status(status, INV_ERR_INVALID_ARG);
     return;
   }
+  if (!INV_SPAN_IN_BOUNDS(status, pos * 64, pos * 64 + 63, (int64_t)max_pos * 64)) return;
   const float2 cv0 = reinterpret_cast<const float2*>(cos_t + pos * 64)[lane];
   const float2 sv0 = reinterpret_cast<const float2*>(sin_t + pos * 64)[lane];
   const float cv[2] = {cv0.x, cv0.y}, sv[2] = {sv0.x, sv0.y};

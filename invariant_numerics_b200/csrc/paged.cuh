@@ -25,6 +25,19 @@ struct RaggedBatch {
   const int32_t* len;      // [n_seqs]
 };
 
+// The entries of the descriptors; every read is checked in the index-checking build.
+__device__ __forceinline__ int start_of(const RaggedBatch& rb, int i, [[maybe_unused]] int* status) {
+  return INV_IN_BOUNDS(status, i, (int64_t)rb.n_seqs + 1) ? rb.q_start[i] : 0;
+}
+__device__ __forceinline__ int len_of(const RaggedBatch& rb, int i, [[maybe_unused]] int* status) {
+  return INV_IN_BOUNDS(status, i, rb.n_seqs) ? rb.len[i] : 0;
+}
+__device__ __forceinline__ int page_of(const RaggedBatch& rb, int i, int64_t j, [[maybe_unused]] int* status) {
+  return INV_IN_BOUNDS(status, j, rb.ld_table) && INV_IN_BOUNDS(status, i, rb.n_seqs)
+             ? rb.page_table[i * rb.ld_table + j]
+             : -1;
+}
+
 // The last i in [0, n) with key(i) <= x, or -1; key ascending.  One warp: each
 // step compares 32 evenly spaced keys, so 32^k candidates take k dependent
 // loads (a binary search would take five times as many).

@@ -181,24 +181,33 @@ struct VerifyArgs {
   int32_t* tokens;
   int32_t* n_accepted;
 };
+// Elements of the buffers, for the index-checking build.
+[[maybe_unused]] __device__ __forceinline__ int64_t target_count(const VerifyArgs& a) {
+  return ((int64_t)a.B * (a.max_draft + 1) - 1) * a.ld_t + a.vocab;
+}
+[[maybe_unused]] __device__ __forceinline__ int64_t draft_count(const VerifyArgs& a) {
+  return ((int64_t)a.B * a.max_draft - 1) * a.ld_d + a.vocab;
+}
 
 // The accepted prefix of sequence b, by one warp, 32 drafts a step: k, or -1 for
 // descriptors out of range; m = number of drafts.
 __device__ __forceinline__ int accepted_prefix(const VerifyArgs& a, int b, int lane, int& m, int* status, bool record) {
   const int D = a.max_draft, V = a.vocab;
-  const int32_t* x = a.draft_tokens + (int64_t)b * D;
-  m = a.n_draft ? a.n_draft[b] : D;
+  m = a.n_draft && INV_IN_BOUNDS(status, b, a.B) ? a.n_draft[b] : D;
   bool bad = m < 0 || m > D;
   int k = bad ? -1 : m;
   for (int i0 = 0; !bad && i0 < m; i0 += 32) {
     const int i = i0 + lane;
     bool ok = true, wrong = false;
-    if (i < m) {
-      const int t = x[i];
+    const int64_t id = (int64_t)b * D + i;
+    if (i < m && INV_IN_BOUNDS(status, id, (int64_t)a.B * D)) {
+      const int t = a.draft_tokens[id];
       wrong = t < 0 || t >= V;
-      if (!wrong) {
-        const double q = a.draft ? (double)a.draft[((int64_t)b * D + i) * a.ld_d + t] : 1.0;
-        ok = (double)a.u_accept[(int64_t)b * D + i] * q < (double)a.target[((int64_t)b * (D + 1) + i) * a.ld_t + t];
+      const int64_t ip = ((int64_t)b * (D + 1) + i) * a.ld_t + t, iq = id * a.ld_d + t;
+      if (!wrong && INV_IN_BOUNDS(status, ip, target_count(a)) &&
+          (!a.draft || INV_IN_BOUNDS(status, iq, draft_count(a)))) {
+        const double q = a.draft ? (double)a.draft[iq] : 1.0;
+        ok = (double)a.u_accept[id] * q < (double)a.target[ip];
       }
     }
     bad = __any_sync(0xffffffffu, wrong);
@@ -210,13 +219,24 @@ __device__ __forceinline__ int accepted_prefix(const VerifyArgs& a, int b, int l
 }
 
 // Everything of the outputs but the next token.
-__device__ __forceinline__ void write_prefix(const VerifyArgs& a, int b, int k) {
+__device__ __forceinline__ void write_prefix(const VerifyArgs& a, int b, int k, [[maybe_unused]] int* status) {
   const int D = a.max_draft;
-  const int32_t* x = a.draft_tokens + (int64_t)b * D;
-  int32_t* out = a.tokens + (int64_t)b * (D + 1);
+  const int64_t id = (int64_t)b * D, io = (int64_t)b * (D + 1);
+  if (!INV_SPAN_IN_BOUNDS(status, io, io + D, (int64_t)a.B * (D + 1)) || !INV_IN_BOUNDS(status, b, a.B)) return;
   for (int i = threadIdx.x; i <= D; i += blockDim.x)
-    if (i != k) out[i] = i < k ? x[i] : -1;
+    if (i != k) a.tokens[io + i] = i < k ? a.draft_tokens[id + i] : -1;
   if (threadIdx.x == 0) a.n_accepted[b] = k < 0 ? 0 : k;
+}
+
+// True if rows p_k and q_k of sequence b and its next token lie in their buffers
+// (always, except in the index-checking build).
+__device__ __forceinline__ bool rows_in_bounds([[maybe_unused]] const VerifyArgs& a, [[maybe_unused]] int b,
+                                               [[maybe_unused]] int k, [[maybe_unused]] int m,
+                                               [[maybe_unused]] int* status) {
+  [[maybe_unused]] const int64_t ip = (int64_t)b * (a.max_draft + 1) + k, iq = (int64_t)b * a.max_draft + k;
+  return INV_IN_BOUNDS(status, ip, (int64_t)a.B * (a.max_draft + 1)) &&
+         INV_SPAN_IN_BOUNDS(status, ip * a.ld_t, ip * a.ld_t + a.vocab - 1, target_count(a)) &&
+         (k >= m || !a.draft || INV_SPAN_IN_BOUNDS(status, iq * a.ld_d, iq * a.ld_d + a.vocab - 1, draft_count(a)));
 }
 
 __device__ __forceinline__ double weight(float p, float q) { return p > q ? (double)p - (double)q : 0.0; }
@@ -249,10 +269,10 @@ __global__ void __launch_bounds__(THR) spec_verify_kernel(const VerifyArgs a, in
   }
   __syncthreads();
   const int k = km[0], m = km[1];
-  if (rank == 0) write_prefix(a, b, k);
+  if (rank == 0) write_prefix(a, b, k, status);
   int32_t* out = a.tokens + (int64_t)b * (D + 1);
   cluster_wait();
-  if (k < 0) return;  // (the same in the whole cluster)
+  if (k < 0 || !rows_in_bounds(a, b, k, m, status)) return;  // (the same in the whole cluster)
   const float* p = a.target + ((int64_t)b * (D + 1) + k) * a.ld_t;
   const float* q = k < m && a.draft ? a.draft + ((int64_t)b * D + k) * a.ld_d : nullptr;
   const int drop = k < m && !a.draft ? a.draft_tokens[(int64_t)b * D + k] : -1;
@@ -390,8 +410,8 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_long_kernel(const 
   }
   __syncthreads();
   const int k = km[0], m = km[1];
-  write_prefix(a, b, k);
-  if (k < 0) return;
+  write_prefix(a, b, k, status);
+  if (k < 0 || !rows_in_bounds(a, b, k, m, status)) return;
   int32_t* out = a.tokens + (int64_t)b * (D + 1);
   const float* p = a.target + ((int64_t)b * (D + 1) + k) * a.ld_t;
   const float* q = k < m && a.draft ? a.draft + ((int64_t)b * D + k) * a.ld_d : nullptr;

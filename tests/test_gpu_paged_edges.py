@@ -256,3 +256,18 @@ def test_the_longest_rows(inv):  # noqa: F811
     t, a = inv.spec_verify(x.zero_().view(1, 1, n), None, none(torch.int32), none(torch.float32),
                            torch.tensor([0.5], device="cuda"))
     assert t.tolist() == [[-1]] and status() == inv.INV_OK
+
+
+def test_the_index_checking_build_agrees_at_the_edges(inv):  # noqa: F811
+    """These tests on the build that checks every index: nothing leaves its buffer."""
+    import os
+    import subprocess
+    import sys
+    from invariant_numerics_b200 import build
+    if inv.inv_debug_bounds_enabled():
+        return  # this is that run
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, INVNUM_LIBRARY=build.build(debug_bounds=True))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", __file__],
+                       cwd=root, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-4000:] + r.stderr[-2000:]

@@ -175,3 +175,27 @@ def test_verify_refuses_more_drafts_than_its_counters_hold(inv):
     f = inv.lib.spec_verify
     for m, want in ((2 ** 31 - 1, INVALID), (2 ** 30 + 1, INVALID), (2 ** 30, OK)):
         assert f(PTR, 100, None, 0, 0, m, 100, PTR, None, PTR, PTR, PTR, PTR, None) == want
+
+
+def test_the_index_checking_build_covers_the_operators(inv):
+    """Every kernel of the paged-cache operators and of verification asks before it reads or writes a caller's buffer,
+    descriptors and page tables included."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "invariant_numerics_b200", "csrc")
+    text = {n: re.sub(r"//.*", "", open(os.path.join(csrc, n)).read())
+            for n in ("paged.cuh", "kv_append.cu", "attn_paged.cu", "sampling.cu")}
+    for name, needs in (("kv_append.cu", ["kv_append_kernel"]),
+                        ("attn_paged.cu", ["attn_few_kernel", "attn_many_kernel", "attn_fold_kernel"]),
+                        ("sampling.cu", ["softmax_kernel", "softmax_long_kernel", "accepted_prefix", "write_prefix",
+                                         "rows_in_bounds"]),
+                        ("paged.cuh", ["start_of", "len_of", "page_of"])):
+        for f in needs:
+            body = re.search(r"\b%s\([^;{]*\{.*?\n\}" % f, text[name], re.S).group(0)
+            assert "_IN_BOUNDS(" in body, f
+    for f in ("spec_verify_kernel", "spec_verify_long_kernel"):
+        body = re.search(r"\b%s\([^;{]*\{.*?\n\}" % f, text["sampling.cu"], re.S).group(0)
+        assert all(g + "(a, b" in body for g in ("accepted_prefix", "write_prefix", "rows_in_bounds")), f
+    # the descriptors are read in these places only
+    for n in ("kv_append.cu", "attn_paged.cu"):
+        assert not re.search(r"\brb\.(q_start|len|page_table)\s*\[", text[n]), n
