@@ -426,9 +426,9 @@ INV_API int prefill_layer(const inv_layer_config* cfg, const inv_layer_weights* 
  * Paged INT16 KV cache ([HEAL] section 1, the codes and scales of the slot
  * cache above).  Codes int16 [n_pages][n_kv_heads][page_size][128], scales
  * fp32 [n_pages][n_kv_heads][page_size], separately for K and V.  page_size is
- * a power of two from 16 to 256.  Position p of sequence i lives in page
- * page_table[i * ld_table + p / page_size] at offset p % page_size; sequences
- * may share pages that neither of them appends to.
+ * a power of two from 16 to 256; scales are >= 0.  Position p of sequence i
+ * lives in page page_table[i * ld_table + p / page_size] at offset p %
+ * page_size; sequences may share pages that neither of them appends to.
  *
  * Ragged batches (kv_append_paged and attn_paged take the same descriptors):
  *   q_start : int32 [n_seqs + 1], ascending; the new tokens of sequence i are
@@ -470,7 +470,9 @@ typedef struct {
  *   q, k heads: rotary embedding as in decode_layer (rotate-half, pairs
  *              (i, i+64), the row's table entries, one fp32 rounding per
  *              product and sum);
- *   k, v heads: quantised as kv_quant_int16 into the row's place in its page.
+ *   k, v heads: quantised as kv_quant_int16 into the row's place in its page
+ *              (a NaN gets code 0 there; the scale is that of the other values,
+ *              NaN where there are none).
  * Without gains the bits are those of decode_layer's QKV step on the same
  * fp32 projections.
  *   qkv    : fp32 [T][ld_qkv], a row holds q (n_heads x 128), k, v (n_kv_heads
@@ -561,7 +563,9 @@ INV_API int softmax_rows(const float* logits, int rows, int n, int64_t ld, float
  *   p_k <= q_k everywhere) the weights are p_k.
  * Comparisons, weights, running sums and totals are in 64 bits.  Without draft
  * probabilities (draft NULL: tokens looked up, not sampled) q_i is 1 at x_i
- * and 0 elsewhere.  No positive weight at all gives the token -1.
+ * and 0 elsewhere.  No positive weight at all gives the token -1.  With NaN, a
+ * comparison fails and a weight is 0: a row of NaN accepts no draft and gives
+ * the token -1.
  *   target : fp32 rows (b, i) at target + (b (max_draft + 1) + i) ld_target.
  *   draft  : fp32 rows (b, i) at draft + (b max_draft + i) ld_draft, or NULL.
  *   draft_tokens : int32 [B][max_draft];  u_accept : fp32 [B][max_draft],

@@ -258,6 +258,52 @@ def test_the_longest_rows(inv):  # noqa: F811
     assert t.tolist() == [[-1]] and status() == inv.INV_OK
 
 
+@pytest.mark.parametrize("V", [500, 5000, 40000, 140000])
+def test_spec_verify_with_nan(inv, V):  # noqa: F811
+    """In every form of the kernel: a NaN accepts nothing and weighs nothing."""
+    p = torch.zeros(4, 2, V, device="cuda")
+    p[:, :, 7], p[:, :, V - 3] = 0.25, 0.75
+    q = torch.zeros(4, 1, V, device="cuda")
+    q[:, :, 7] = 1.0
+    p[0, 0] = math.nan   # a target row of nothing else
+    q[1, 0, 7] = math.nan  # at the draft: rejected; no residual there, and q is 0 at V - 3
+    q[2, 0] = math.nan   # no residual at all: the target's own weights
+    p[3, 0, 7] = math.nan  # rejected, without weight
+    x = torch.full((4, 1), 7, dtype=torch.int32, device="cuda")
+    zero, low = torch.zeros(4, 1, device="cuda"), torch.full((4,), 0.1, device="cuda")
+    t, a = inv.spec_verify(p, q, x, zero, low)
+    assert a.tolist() == [0] * 4 and t.tolist() == [[-1, -1], [V - 3, -1], [7, -1], [V - 3, -1]]
+    t, a = inv.spec_verify(p, None, x, zero, low)  # looked-up drafts: accepted with u = 0 where p is a number
+    assert a.tolist() == [0, 1, 1, 0] and t.tolist() == [[-1, -1], [7, 7], [7, 7], [V - 3, -1]]
+    assert status() == inv.INV_OK
+
+
+def test_kv_append_paged_with_nan(inv):  # noqa: F811
+    """NaN in a key or value row: the codes and scales of kv_quant_int16; in a query: NaN."""
+    hq, hkv, page, T = 4, 2, 16, 3
+    n_pages, table, start, ln = batch([T], [T], page, seed=92)
+    x = torch.randn(T, (hq + 2 * hkv) * 128, generator=gen(93), device="cuda")
+    x[0, 5] = x[1, hq * 128 + 9] = x[2, (hq + hkv) * 128 + 100] = math.nan
+    x[2, (hq + hkv + 1) * 128:] = math.nan  # a whole value row
+    cos, sin = torch.ones(8, 64, device="cuda"), torch.zeros(8, 64, device="cuda")
+    cache, slot = inv.PagedKVCache.empty(n_pages, hkv, page), inv.KVCache(n_slots=1, n_kv_heads=hkv, max_len=16)
+    q = inv.kv_append_paged(x, cache, table, start, ln, cos, sin)
+    assert torch.isnan(q[0, 0, [5, 69]]).all() and int(torch.isnan(q).sum()) == 2
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    y = x.view(T, -1, 128)
+    k = y[:, hq:hq + hkv].clone()
+    k[1, 0, 9] = k[1, 0, 73] = math.nan  # the rotated pair: x 1 - NaN 0
+    inv.kv_quant_int16(k.contiguous(), torch.zeros_like(pos), pos, slot, "k")
+    inv.kv_quant_int16(y[:, hq + hkv:].contiguous(), torch.zeros_like(pos), pos, slot, "v")
+    pg = int(table[0, 0])
+    bits = lambda t: t.view(torch.int32) if t.dtype == torch.float32 else t
+    for a, b in ((cache.k, slot.k), (cache.v, slot.v), (cache.k_scale, slot.k_scale), (cache.v_scale, slot.v_scale)):
+        assert torch.equal(bits(a)[pg, :, :T], bits(b)[0, :, :T])
+    # fmax keeps the number beside a NaN, and a NaN of two
+    assert torch.isnan(cache.v_scale[pg, 1, 2]) and int(torch.isnan(cache.v_scale).sum()) == 1
+    assert not torch.isnan(cache.k_scale).any() and status() == inv.INV_OK
+
+
 def test_the_index_checking_build_agrees_at_the_edges(inv):  # noqa: F811
     """These tests on the build that checks every index: nothing leaves its buffer."""
     import os
