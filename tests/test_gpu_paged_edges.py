@@ -199,6 +199,42 @@ def test_lengths_next_to_two_to_the_31(inv):  # noqa: F811
         assert status() == inv.INV_ERR_INVALID_ARG and (out == 5.0).all()
 
 
+def test_long_contexts_at_the_end_of_a_large_cache(inv):  # noqa: F811
+    """Contexts of 33000 and 40003 positions in pages whose codes lie beyond element 2^31 of the cache, rows before the
+    first sequence: float64, and the bits of the same pages in a small cache; what append writes too."""
+    hq, hkv, page = 16, 8, 256
+    lens, news, skip = [40003, 33000, 36000], [1, 70, 3], 2
+    n_pages, table, start, ln = batch(lens, news, page, seed=94)
+    small = pool(inv, n_pages, hkv, page, seed=95)
+    total = 8200 + n_pages  # 8192 pages hold 2^31 codes
+    shape = (total, hkv, page, 128)
+    large = inv.PagedKVCache(*(torch.empty(shape, dtype=torch.int16, device="cuda") for _ in range(2)),
+                             *(torch.full(shape[:3], math.nan, device="cuda") for _ in range(2)))
+    names = ("k", "v", "k_scale", "v_scale")
+    for name in names:
+        getattr(large, name)[total - n_pages:] = getattr(small, name)
+    far = torch.where(table >= 0, table + (total - n_pages), table)
+    start = start + skip
+    T = int(start[-1])
+    x = torch.randn(T, (hq + 2 * hkv) * 128, generator=gen(96), device="cuda")
+    cos, sin = tables(inv, 40960)
+    q = inv.kv_append_paged(x, small, table, start, ln, cos, sin)
+    q2 = inv.kv_append_paged(x, large, far, start, ln, cos, sin)
+    assert torch.equal(q[skip:], q2[skip:])
+    for name in names:
+        assert torch.equal(getattr(large, name)[total - n_pages:], getattr(small, name))
+        if "scale" in name:
+            assert torch.isnan(getattr(large, name)[:total - n_pages]).all()
+    q = torch.where(torch.isfinite(q), q, torch.zeros_like(q)) * 0.3
+    q[:skip] = math.nan  # rows of no sequence
+    out, out2 = torch.full_like(q, 3.0), torch.full_like(q, 3.0)
+    inv.attn_paged(q, small, table, start, ln, SCALE, max_len_bound=40960, out=out)
+    inv.attn_paged(q, large, far, start, ln, SCALE, out=out2)
+    assert torch.equal(out, out2) and (out[:skip] == 3.0).all()
+    check_attend(inv, q, small, table, start, ln, out, rows=slice(skip, T))
+    assert status() == inv.INV_OK
+
+
 # ------------------------------------------------------------------ softmax ---
 
 @pytest.mark.parametrize("n", [1, 5, 1000, 8192, 8193, 16385, 65536, 65537, 131073, 262144, 262145, 300001])
