@@ -504,11 +504,18 @@ INV_API int kv_append_paged(const float* qkv, int64_t ld_qkv, int T, int n_heads
  *   blocks are joined by a running maximum inside segments of
  *   INV_PAGED_SEGMENT keys, and segments, in ascending order, the same way.
  *   q        : fp32 [T][ld_q], n_heads x 128 used; ld_q % 4 == 0, 16-byte aligned.
+ *   K scales : below 2^92 (keys below 1e32); beyond, scores leave fp32 and the
+ *              rows that see such a key get unspecified values.
  *   out      : fp32 [T][n_heads][128]; out_hi/out_lo: binary16 split of out
- *              (both NULL or both non-NULL).
+ *              (both NULL or both non-NULL).  They may not overlap q.
  *   max_q_bound : host upper bound on the new tokens of a sequence (<= 0: T).
  *   max_len_bound : host upper bound on every len[i] (<= 0: ld_table *
- *              page_size), at most 2^31 - 512 as a len is.  The bounds size the launch and the workspace only.
+ *              page_size), at most 2^31 - 512 as a len is.  The bounds size the
+ *              launch and the workspace and change no bits, but loose ones cost
+ *              time: 128 tokens of their own over 2048 keys each, 32 / 8 heads,
+ *              take 241 us with exact bounds, 326 with 32768, 1299 with 18944
+ *              (segments that divide 2 SMs / n_kv_heads fall to the same CTAs),
+ *              257 with 2048 and without max_q_bound.
  *   softmax_scale : sigma >= 0, finite.
  *   workspace: attn_paged_workspace_size(...) bytes for the resolved bounds (on
  *              the device of the call: the size depends on its number of SMs),

@@ -230,13 +230,18 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 // An item is computed by the code for its number of tiles of 8 rows, so a decode row
 // in a call with prompts or drafts costs what it costs alone (128 x 2048 keys 235 us;
 // with the code of four tiles 527, with its idle tiles skipped at run time 361).
-// Measured (32 query, 8 kv heads): 128 sequences of 2048 keys 232 us (4.73 TB/s of
-// codes, scales and q; without its products 188), 64 of up to 8192 289 us; 32
+// Measured (32 query, 8 kv heads; replays of a graph of the calls, a call among others
+// from Python takes 252 us for the first): 128 sequences of 2048 keys 231 us (4.73 TB/s of
+// codes, scales and q; without its products 188), 64 of up to 8192 290 us; 32
 // sequences over 4096 keys: 4 tokens 183, 5 tokens 237, 8 tokens 297.  Not HBM but the
 // warps bound it: loads from shared memory, unpacking, two barriers a block; from
 // three tiles on the MMAs' and the softmax's latency too, at two CTAs a SM.  Four warps
 // of two m-tiles (264 us for the first case), half-block slots (278) and one CTA a SM
 // with four slots (278) were slower.
+// The items go round in their order, empty ones included, which a bound far above the
+// lengths makes many of (the first case with a bound of 131072: 615 us).  Where the bound's
+// number of segments divides gridDim.x / heads, a CTA meets the same segment in every
+// sequence: 37 segments, of which 4 hold keys, 1299 us.
 constexpr int MAX_NT = 4;  // tiles of 8 rows of an item
 constexpr int FEW_WARPS = 8, FEW_T = 32 * FEW_WARPS;
 constexpr int TH = FEW_T + 32;
@@ -714,9 +719,9 @@ __global__ void __launch_bounds__(TH, 2)
 // Tensor memory (512 columns): Q hi | Q lo (64 each), two score blocks (128
 // each, W in place of the scores), O (128).
 // Each product is three chains of 8 MMAs (hi lo, lo hi, hi hi) of 64 clocks, two
-// products a block.  Measured: a prompt of 8192 tokens (32 query, 8 kv heads) 2.26 ms,
-// 243 TFLOP/s of useful products and three times that executed, 0.44 of the dense
-// rate.  Two chains of about 8K clocks a block bound it, which overlap each other
+// products a block.  Measured: a prompt of 8192 tokens (32 query, 8 kv heads) 2.24 ms in
+// a graph, 2.32 as a call: 245 TFLOP/s of useful products and three times that executed,
+// 0.45 of the dense rate.  Two chains of about 8K clocks a block bound it, which overlap each other
 // and the MMAs: the softmax warps', and unpacking V with the product behind it.
 // 16 softmax warps (2.70 ms), separate converters for K and V (2.43) and folding O
 // in before the weights (2.30) were slower.

@@ -9,13 +9,13 @@ using inv::record_status;
 constexpr int kAppendThreads = 256;
 
 // HBM bound (a row reads 512 bytes a head, writes 512 a query and 260 a key or
-// value head).  One CTA per row (and one that checks q_start), one warp per head (warp w takes heads w, w + 8,
-// ...).  Lane l holds the dims 2l, 2l+1, 64+2l, 65+2l, so a rotary pair (i, i+64) is
+// value head).  One CTA per row, and one that checks q_start; one warp per head (warp w
+// takes heads w, w + 8, ...).  Lane l holds the dims 2l, 2l+1, 64+2l, 65+2l, so a rotary pair (i, i+64) is
 // in one lane and a warp's loads are two contiguous 256-byte runs.  A warp requests
 // kBatch heads before it looks up the row's sequence, position and page (three
-// dependent reads), so that both latencies overlap: 69 us for 8192 rows (32 query, 8
-// kv heads) = 5.4 TB/s, 78 with the look-ups first; 5.5 us for 64 sequences of up to
-// 5 tokens.
+// dependent reads), so that both latencies overlap: 70 us for 8192 rows (32 query, 8
+// kv heads) = 5.3 TB/s, 78 with the look-ups first; 5.6 us for 64 sequences of up to
+// 5 tokens.  (q_start checked by every row's CTA: 3 us more for the 8192.)
 constexpr int kBatch = 6;
 
 __global__ void __launch_bounds__(kAppendThreads)
